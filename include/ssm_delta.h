@@ -1,0 +1,99 @@
+/*
+ * ssm_delta.h -- the gated delta rule, exported by libssmscan.so.
+ *
+ * A recurrence with a matrix state, like the scalar-decay heads of
+ * ssm_ssd_fwd, whose update first takes back what the state already predicts
+ * for the step's key.  Per batch row and value head, with the state S (V x K),
+ * the key head of a value head h being h / (Hv / Hk):
+ *
+ *   u_t = beta_t (v_t - exp(g_t) S_{t-1} k_t)
+ *   S_t = exp(g_t) S_{t-1} + u_t k_t^T,          S_{-1} = h0, or 0
+ *   y_t = scale S_t q_t                          (the post-update state)
+ *
+ * The conventions (ownership, streams, no host synchronisation, validation
+ * before any HIP call, status codes) are those of ssm_scan.h.
+ */
+#ifndef SSM_DELTA_H
+#define SSM_DELTA_H
+
+#include "ssm_scan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    int64_t batch;     /* B >= 1 */
+    int64_t seqlen;    /* L >= 1 (1 for ssm_delta_step) */
+    int64_t kheads;    /* Hk >= 1, heads of q and k */
+    int64_t vheads;    /* Hv, a multiple of Hk: heads of v, g, beta and y */
+    int64_t dkey;      /* K, 1 <= K <= 128 */
+    int64_t dvalue;    /* V, 1 <= V <= 1024 */
+    float scale;       /* of the output; finite */
+    int32_t io_dtype;  /* ssm_dtype_t of q, k, v, g, beta, y and of their gradients */
+} ssm_delta_desc_t;
+
+/* Bytes of workspace ssm_delta_fwd and ssm_delta_bwd need for `desc`; 0 for an
+ * invalid or unsupported descriptor.  Both grow with B * ceil(L / 64). */
+size_t ssm_delta_workspace_bytes(const ssm_delta_desc_t *desc);
+size_t ssm_delta_bwd_workspace_bytes(const ssm_delta_desc_t *desc);
+
+/*
+ * The whole sequence, 64 steps at a time on the matrix units.
+ *
+ *   q, k     [B][L][Hk][K]  io dtype   queries and keys (a key longer than 1 with
+ *                                      beta near 1 makes the recurrence itself unstable)
+ *   v        [B][L][Hv][V]  io dtype
+ *   g        [B][L][Hv]     io dtype   log decay; -infinity (any g <= -10000) clears the state
+ *   beta     [B][L][Hv]     io dtype
+ *   h0       [B][Hv][V][K]  fp32, or NULL   state before step 0 (NULL: 0)
+ *   lengths  [B]            int32, or NULL  steps of each row that count, clamped to [0, L]
+ *                                      (NULL: L).  Later rows of q, k, v, g and beta are not
+ *                                      read, and those of y are left as they were.
+ *   y        [B][L][Hv][V]  io dtype   output (written)
+ *   h_last   [B][Hv][V][K]  fp32, or NULL   state behind each row's last step (written)
+ *   workspace  ssm_delta_workspace_bytes(desc) bytes, 256-byte aligned
+ *
+ * The state, its products and sums are held to fp32 for either io dtype; no
+ * atomics, so equal calls give equal bits.  Every pointer is aligned to its
+ * element size; rows that are multiples of 16 bytes at 16-byte aligned
+ * pointers move fastest.  h_last may not alias h0.  Returns an ssm_status_t.
+ */
+int ssm_delta_fwd(const ssm_delta_desc_t *desc, const void *q, const void *k, const void *v, const void *g,
+                  const void *beta, const float *h0, const int32_t *lengths, void *y, float *h_last,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One step with the state updated in place (decoding): the tensors of
+ * ssm_delta_fwd without their time axis, q, k [B][Hk][K], v, y [B][Hv][V],
+ * g, beta [B][Hv], and h [B][Hv][V][K] fp32, read as S_{t-1} and overwritten
+ * with S_t.  desc->seqlen must be 1.  No workspace.
+ */
+int ssm_delta_step(const ssm_delta_desc_t *desc, const void *q, const void *k, const void *v, const void *g,
+                   const void *beta, float *h, void *y, void *stream);
+
+/*
+ * Gradients of sum(dy * y) + <dh_last, h_last> with y, h_last from
+ * ssm_delta_fwd on the same inputs.  The states entering each chunk are
+ * computed again and kept in the workspace.
+ *
+ *   dy       [B][L][Hv][V] io dtype        (rows behind a row's length are not read)
+ *   dh_last  [B][Hv][V][K] fp32, or NULL   (NULL: 0)
+ * outputs, all required but dh0; rows behind a row's length are written as 0:
+ *   dq, dk   [B][L][Hk][K] io dtype        sums over the value heads of a key head
+ *   dv       [B][L][Hv][V] io dtype
+ *   dg, dbeta [B][L][Hv]   io dtype        (dg is 0 where g <= -10000)
+ *   dh0      [B][Hv][V][K] fp32, or NULL   gradient of the state before step 0
+ *   workspace  ssm_delta_bwd_workspace_bytes(desc) bytes, 256-byte aligned
+ * Sums are taken in fp32 in a fixed order.  Returns an ssm_status_t.
+ */
+int ssm_delta_bwd(const ssm_delta_desc_t *desc, const void *q, const void *k, const void *v, const void *g,
+                  const void *beta, const float *h0, const int32_t *lengths, const void *dy, const float *dh_last,
+                  void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSM_DELTA_H */

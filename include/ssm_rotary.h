@@ -1,0 +1,55 @@
+/*
+ * ssm_rotary.h -- rotary positions, exported by libssmscan.so.
+ *
+ * Each pair (a, b) of a head is turned by the angle t = p * inv_freq[i] of its
+ * position p and pair index i, and scaled:
+ *
+ *   (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t)
+ *
+ * Turning B and C (or q and k) by position before a recurrence with a real
+ * state is the complex state of ssm_scan_fwd with a constant angle per step.
+ * The angle is formed and reduced in 64 bits, so positions of millions keep
+ * fp32 accuracy.  Scaled forms for long contexts are choices of inv_freq and
+ * amplitude.  Conventions and status codes are those of ssm_scan.h.
+ */
+#ifndef SSM_ROTARY_H
+#define SSM_ROTARY_H
+
+#include "ssm_scan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    int64_t batch;        /* B >= 1 */
+    int64_t seqlen;       /* L >= 1 */
+    int64_t qheads;       /* Hq >= 1 */
+    int64_t kheads;       /* Hk >= 0; 0 when k is NULL */
+    int64_t dhead;        /* K, 2 <= K <= 65536 */
+    int64_t rotary;       /* R, even, 2 <= R <= K: the leading elements of a head that are turned */
+    int64_t offset;       /* added to every position */
+    float amplitude;      /* finite */
+    int32_t interleaved;  /* pairs (2i, 2i + 1) if 1, (i, i + R/2) if 0 */
+    int32_t inverse;      /* 1: by the angle -t, which is the gradient's direction */
+    int32_t io_dtype;     /* ssm_dtype_t of q, k and the outputs */
+} ssm_rotary_desc_t;
+
+/*
+ *   q          [B][L][Hq][K] io dtype
+ *   k          [B][L][Hk][K] io dtype, or NULL (with kheads 0)
+ *   inv_freq   [R / 2] fp32
+ *   positions  [B][L] int64, or NULL: 0 .. L-1 (desc->offset is added either way)
+ *   q_out, k_out  like q and k (written); each may be its input itself, and
+ *              overlaps nothing else
+ * With inverse = 1 the call maps gradients of the outputs to gradients of the
+ * inputs.  The elements behind R are copied.  Returns an ssm_status_t.
+ */
+int ssm_rotary(const ssm_rotary_desc_t *desc, const void *q, const void *k, const float *inv_freq,
+               const int64_t *positions, void *q_out, void *k_out, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSM_ROTARY_H */

@@ -22,8 +22,8 @@ LIB = os.path.join(PKG, "libssmscan.so")
 # ordering test of the chunked kernel's decoupled look-back loads it)
 LOOKBACK_TEST_LIB = os.path.join(PKG, "libssmscan_lookback_test.so")
 LOOKBACK_TEST_DELAY = 12
-SOURCES = [os.path.join(CSRC, "ssm_scan.hip"), os.path.join(CSRC, "mimo.hip"), os.path.join(CSRC, "calibrate.hip")]
-HEADERS = [os.path.join(ROOT, "include", "ssm_scan.h"), os.path.join(ROOT, "include", "ssm_calibrate.h")] + [
+SOURCES = [os.path.join(CSRC, f) for f in ("ssm_scan.hip", "mimo.hip", "delta.hip", "rotary.hip", "calibrate.hip")]
+HEADERS = [os.path.join(ROOT, "include", f) for f in ("ssm_scan.h", "ssm_delta.h", "ssm_rotary.h", "ssm_calibrate.h")] + [
     os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".h")]
 ARCH = os.environ.get("SSM_OFFLOAD_ARCH", "gfx950")
 

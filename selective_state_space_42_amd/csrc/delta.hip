@@ -1,0 +1,220 @@
+// delta.hip -- host side of include/ssm_delta.h: argument checks, workspace
+// layout and launches of the gated delta rule's kernels.
+#include "ssm_delta.h"
+
+#include "host_common.h"
+#include "kernel_delta.h"
+#include "kernel_delta_bwd.h"
+
+namespace {
+
+using namespace ssm::delta;
+
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+
+int check_desc(const ssm_delta_desc_t* d) {
+    if (!d) return SSM_ERR_INVALID_ARGUMENT;
+    if (d->batch < 1 || d->seqlen < 1 || d->kheads < 1 || d->vheads < 1 || d->dkey < 1 || d->dvalue < 1)
+        return SSM_ERR_INVALID_ARGUMENT;
+    if (d->vheads % d->kheads || !ssm::finite(d->scale)) return SSM_ERR_INVALID_ARGUMENT;
+    if (d->io_dtype != SSM_DTYPE_F32 && d->io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
+    if (d->dkey > 128 || d->dvalue > 1024) return SSM_ERR_UNSUPPORTED;
+    if (!ssm::product_fits({d->batch, d->seqlen, d->vheads, 1024}, kMaxElements) ||
+        !ssm::product_fits({d->batch, (d->seqlen + kC - 1) / kC, d->vheads, (d->dvalue + 15) / 16}, INT32_MAX))
+        return SSM_ERR_INVALID_ARGUMENT;
+    return SSM_OK;
+}
+
+struct Layout {
+    size_t kf, ktf, qf, qtf, xf, xtf, pf, ptf, vec, states, news, after, dr, total;
+};
+
+Layout layout(const ssm_delta_desc_t* d, bool bwd) {
+    Layout o{};
+    const size_t nC = (d->seqlen + kC - 1) / kC, in = d->io_dtype == SSM_DTYPE_F32 ? 3 : 1;
+    const size_t kc = d->batch * d->kheads * nC, vc = d->batch * d->vheads * nC;
+    const size_t KP = (d->dkey + 31) / 32 * 32, VP = (d->dvalue + 31) / 32 * 32;
+    const auto take = [&o](size_t& at, size_t bytes) {
+        at = o.total;
+        o.total += (bytes + 255) / 256 * 256;
+    };
+    const size_t rows = kc * in * (KP / 8) * kFrag * 2;
+    take(o.kf, rows);
+    take(o.ktf, rows);
+    take(o.qf, rows);
+    take(o.xf, vc * 3 * kTri * kFrag * 2);
+    take(o.vec, vc * 3 * kC * 4);
+    if (!bwd) {
+        take(o.pf, vc * (in == 3 ? 3 : 2) * kTri * kFrag * 2);
+        return o;
+    }
+    take(o.qtf, rows);
+    take(o.xtf, vc * 3 * kTri * kFrag * 2);
+    take(o.ptf, vc * 3 * kTri * kFrag * 2);
+    take(o.states, vc * KP * VP * 4);
+    take(o.after, vc * KP * VP * 4);
+    take(o.news, vc * kC * VP * 4);
+    take(o.dr, vc * kC * VP * 4);
+    return o;
+}
+
+Params params(const ssm_delta_desc_t* d, const Layout& o, bool bwd, void* workspace) {
+    Params p{};
+    char* w = static_cast<char*>(workspace);
+    const auto u16 = [w](size_t at) { return reinterpret_cast<uint16_t*>(w + at); };
+    const auto f32 = [w](size_t at) { return reinterpret_cast<float*>(w + at); };
+    p.kf = u16(o.kf); p.ktf = u16(o.ktf); p.qf = u16(o.qf); p.xf = u16(o.xf); p.vec = f32(o.vec);
+    if (bwd) {
+        p.qtf = u16(o.qtf); p.xtf = u16(o.xtf); p.ptf = u16(o.ptf);
+        p.states = f32(o.states); p.news = f32(o.news);
+    } else {
+        p.pf = u16(o.pf);
+    }
+    p.B = d->batch; p.L = d->seqlen; p.Hk = d->kheads; p.Hv = d->vheads; p.K = d->dkey; p.V = d->dvalue;
+    p.nC = (d->seqlen + kC - 1) / kC;
+    p.VP = (d->dvalue + 31) / 32 * 32;
+    p.nV = bwd ? p.VP / 16 : (d->dvalue + 15) / 16;
+    p.scale = d->scale;
+    return p;
+}
+
+dim3 grid(int64_t n) { return dim3(static_cast<unsigned>(n)); }
+
+template <typename T, int KS>
+int fwd(const Params& p, hipStream_t s) {
+    hipLaunchKernelGGL((delta_pack_kernel<T, KS, false>), grid(p.B * p.Hk * p.nC), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_solve_kernel<T, KS, false>), grid(p.B * p.Hv * p.nC), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, true>), grid(p.B * p.Hv * p.nV), dim3(64), 0, s, p);
+    return ssm::launch_status();
+}
+
+template <typename T, int KS>
+int bwd(const GradParams& g, hipStream_t s) {
+    const Params& p = g.f;
+    hipLaunchKernelGGL((delta_pack_kernel<T, KS, true>), grid(p.B * p.Hk * p.nC), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_solve_kernel<T, KS, true>), grid(p.B * p.Hv * p.nC), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, false>), grid(p.B * p.Hv * p.nV), dim3(64), 0, s, p);
+    hipLaunchKernelGGL((delta_adjoint_kernel<T, KS>), grid(p.B * p.Hv * p.nV), dim3(64), 0, s, g);
+    hipLaunchKernelGGL((delta_grad_kernel<T, KS>), grid(p.B * p.Hk * p.nC), dim3(256), 0, s, g);
+    return ssm::launch_status();
+}
+
+template <typename T>
+int step(const StepParams& p, bool vec, hipStream_t s) {
+    const int np = static_cast<int>((p.K + 31) / 32);
+    const dim3 g = grid(p.B * p.Hv * p.row_blocks);
+#define SSM_STEP(N)                                                                                 \
+    case N:                                                                                         \
+        if (vec)                                                                                    \
+            hipLaunchKernelGGL((delta_step_kernel<T, N, true>), g, dim3(256), 0, s, p);             \
+        else                                                                                        \
+            hipLaunchKernelGGL((delta_step_kernel<T, N, false>), g, dim3(256), 0, s, p);            \
+        break;
+    switch (np) {
+        SSM_STEP(1)
+        SSM_STEP(2)
+        SSM_STEP(3)
+        SSM_STEP(4)
+    }
+#undef SSM_STEP
+    return ssm::launch_status();
+}
+
+// every K of 1 .. 128 runs the kernels of its multiple of 32
+template <template <typename, int> class Op, typename P>
+int by_size(const ssm_delta_desc_t* d, const P& p, hipStream_t s) {
+    const int ks = static_cast<int>((d->dkey + 31) / 32);
+    if (d->io_dtype == SSM_DTYPE_F32)
+        return ks == 1 ? Op<float, 1>::run(p, s) : ks == 2 ? Op<float, 2>::run(p, s)
+             : ks == 3 ? Op<float, 3>::run(p, s) : Op<float, 4>::run(p, s);
+    return ks == 1 ? Op<uint16_t, 1>::run(p, s) : ks == 2 ? Op<uint16_t, 2>::run(p, s)
+         : ks == 3 ? Op<uint16_t, 3>::run(p, s) : Op<uint16_t, 4>::run(p, s);
+}
+
+template <typename T, int KS>
+struct Fwd {
+    static int run(const Params& p, hipStream_t s) { return fwd<T, KS>(p, s); }
+};
+template <typename T, int KS>
+struct Bwd {
+    static int run(const GradParams& p, hipStream_t s) { return bwd<T, KS>(p, s); }
+};
+
+bool misaligned(std::initializer_list<const void*> ps, size_t a) {
+    for (const void* x : ps)
+        if (x && !ssm::aligned(x, a)) return true;
+    return false;
+}
+
+size_t io_size(const ssm_delta_desc_t* d) { return d->io_dtype == SSM_DTYPE_F32 ? 4 : 2; }
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_delta_workspace_bytes(const ssm_delta_desc_t* d) {
+    return check_desc(d) == SSM_OK ? layout(d, false).total : 0;
+}
+
+size_t ssm_delta_bwd_workspace_bytes(const ssm_delta_desc_t* d) {
+    return check_desc(d) == SSM_OK ? layout(d, true).total : 0;
+}
+
+int ssm_delta_fwd(const ssm_delta_desc_t* d, const void* q, const void* k, const void* v, const void* g,
+                  const void* beta, const float* h0, const int32_t* lengths, void* y, float* h_last, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+    const int st = check_desc(d);
+    if (st != SSM_OK) return st;
+    if (!q || !k || !v || !g || !beta || !y) return SSM_ERR_INVALID_ARGUMENT;
+    if (misaligned({q, k, v, g, beta, y}, io_size(d)) || misaligned({h0, lengths, h_last}, 4))
+        return SSM_ERR_INVALID_ARGUMENT;
+    if (h0 && h0 == h_last) return SSM_ERR_INVALID_ARGUMENT;
+    const Layout o = layout(d, false);
+    if (!workspace || workspace_bytes < o.total) return SSM_ERR_WORKSPACE_TOO_SMALL;
+    if (!ssm::aligned(workspace, 256)) return SSM_ERR_INVALID_ARGUMENT;
+    Params p = params(d, o, false, workspace);
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.h0 = h0; p.lengths = lengths; p.y = y; p.h_last = h_last;
+    return by_size<Fwd>(d, p, static_cast<hipStream_t>(stream));
+}
+
+int ssm_delta_step(const ssm_delta_desc_t* d, const void* q, const void* k, const void* v, const void* g,
+                   const void* beta, float* h, void* y, void* stream) {
+    const int st = check_desc(d);
+    if (st != SSM_OK) return st;
+    if (d->seqlen != 1) return SSM_ERR_INVALID_ARGUMENT;
+    if (!q || !k || !v || !g || !beta || !h || !y) return SSM_ERR_INVALID_ARGUMENT;
+    if (misaligned({q, k, v, g, beta, y}, io_size(d)) || misaligned({h}, 4)) return SSM_ERR_INVALID_ARGUMENT;
+    StepParams p{};
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.h = h; p.y = y;
+    p.B = d->batch; p.Hk = d->kheads; p.Hv = d->vheads; p.K = d->dkey; p.V = d->dvalue;
+    p.row_blocks = (d->dvalue + 31) / 32;
+    p.scale = d->scale;
+    const bool vec = d->dkey % 4 == 0 && ssm::aligned(h, 16);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return d->io_dtype == SSM_DTYPE_F32 ? step<float>(p, vec, s) : step<uint16_t>(p, vec, s);
+}
+
+int ssm_delta_bwd(const ssm_delta_desc_t* d, const void* q, const void* k, const void* v, const void* g,
+                  const void* beta, const float* h0, const int32_t* lengths, const void* dy, const float* dh_last,
+                  void* dq, void* dk, void* dv, void* dg, void* dbeta, float* dh0, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+    const int st = check_desc(d);
+    if (st != SSM_OK) return st;
+    if (!q || !k || !v || !g || !beta || !dy || !dq || !dk || !dv || !dg || !dbeta) return SSM_ERR_INVALID_ARGUMENT;
+    if (misaligned({q, k, v, g, beta, dy, dq, dk, dv, dg, dbeta}, io_size(d)) ||
+        misaligned({h0, lengths, dh_last, dh0}, 4))
+        return SSM_ERR_INVALID_ARGUMENT;
+    const Layout o = layout(d, true);
+    if (!workspace || workspace_bytes < o.total) return SSM_ERR_WORKSPACE_TOO_SMALL;
+    if (!ssm::aligned(workspace, 256)) return SSM_ERR_INVALID_ARGUMENT;
+    GradParams p{};
+    p.f = params(d, o, true, workspace);
+    p.f.q = q; p.f.k = k; p.f.v = v; p.f.g = g; p.f.beta = beta; p.f.h0 = h0; p.f.lengths = lengths;
+    p.dy = dy; p.dh_last = dh_last; p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.dh0 = dh0;
+    p.after = reinterpret_cast<float*>(static_cast<char*>(workspace) + o.after);
+    p.dr = reinterpret_cast<float*>(static_cast<char*>(workspace) + o.dr);
+    p.vec_v = d->dvalue * io_size(d) % 16 == 0 && ssm::aligned(dy, 16);
+    return by_size<Bwd>(d, p, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,39 @@
+// host_common.h -- small host helpers of the C entry points.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+namespace ssm {
+
+// SSM_OK, or SSM_ERR_HIP with the error kept for ssm_scan_last_hip_error (ssm_scan.hip)
+int hip_status(hipError_t e);
+
+inline int launch_status() { return hip_status(hipGetLastError()); }
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+inline bool finite(float x) { return x - x == 0.f; }
+
+// whether the product of non-negative factors stays at or below `most`
+inline bool product_fits(std::initializer_list<int64_t> factors, int64_t most) {
+    int64_t r = 1;
+    for (const int64_t f : factors)
+        if (__builtin_mul_overflow(r, f, &r) || r > most) return false;
+    return true;
+}
+
+struct Range {
+    const void* base;
+    uint64_t bytes;
+};
+
+inline bool overlap(const Range& a, const Range& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.base), y = reinterpret_cast<uintptr_t>(b.base);
+    return a.base && b.base && x < y + b.bytes && y < x + a.bytes;
+}
+
+}  // namespace ssm

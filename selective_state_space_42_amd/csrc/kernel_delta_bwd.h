@@ -1,0 +1,386 @@
+// kernel_delta_bwd.h -- gradients of the gated delta rule.
+//
+// With the forward's notation (kernel_delta.h), dS' the gradient of the state
+// behind a chunk and o elementwise by rows:
+//   dU = P^T dY + e^{G_63 - G} o (K dS')
+//   dR = (I - X^T D) dU,  dE = beta o dR = dV,  dbeta = rows of dR . E^
+//   dS = e^{G_63} dS' + (scale e^G o Q)^T dY - (e^G o K)^T dE
+// runs backwards over the chunks (delta_adjoint_kernel, the mirror of
+// delta_chunk_kernel), after a forward sweep that keeps the states entering
+// the chunks and E^.  Everything else is a chunk's own (delta_grad_kernel):
+//   W1_ij = e^{G_i - G_j} dY_i . U_j (j <= i),   W2_ij = e^{G_i - G_j} dE_i . U_j (j < i)
+//   dQ  = scale (e^G o (dY S^T) + W1 K)
+//   row = -(e^G o (dE S^T) + W2 K),   col = scale W1^T Q - W2^T K + over,  over = e^{G_63 - G} o (U dS'^T)
+//   dK  = row + col
+// G_i enters wherever q_i or k_i predicts (e^{G_i}) and, negated, wherever k_i
+// is written (e^{-G_i}), so its gradient is q_i.dQ_i + k_i.row_i - k_i.col_i,
+// and that of the chunk's end adds sum_j k_j.over_j + e^{G_63} <dS', S>; dg is
+// the sum of these from each step to the chunk's end.
+#pragma once
+
+#include "kernel_delta.h"
+
+namespace ssm {
+namespace delta {
+
+struct GradParams {
+    Params f;
+    const void* dy;
+    const float* dh_last;
+    void *dq, *dk, *dv, *dg, *dbeta;
+    float* dh0;
+    float *after, *dr;  // gradients of the states behind each chunk (K x VP), dR of each step (64 x VP)
+    int32_t vec_v;      // rows of dy move in 16-byte pieces
+};
+
+template <typename T, int KS>
+__global__ void __launch_bounds__(64) delta_adjoint_kernel(GradParams gp) {
+    constexpr int kN = PlanesOf<T>::kIn;
+    const Params& p = gp.f;
+    const int lane = threadIdx.x, q = lane >> 4;
+    const int64_t VP = p.VP, vt = blockIdx.x % p.nV, bh = blockIdx.x / p.nV, b = bh / p.Hv, h = bh % p.Hv;
+    const int64_t col = vt * 16 + (lane & 15);
+    const bool ok = col < p.V;
+    const int64_t len = row_len(p.lengths, b, p.L), chunks = (len + kC - 1) / kC;
+    f32x4 S[2 * KS];
+    load_state<KS>(gp.dh_last ? gp.dh_last + (bh * p.V + (ok ? col : 0)) * p.K : nullptr, p.K, ok, lane, S);
+    const T* dy = static_cast<const T*>(gp.dy);
+    T* dv = static_cast<T*>(gp.dv);
+    const int64_t kunit = static_cast<int64_t>(kN) * 4 * KS * kFrag;
+    const int64_t kat = (b * p.Hk + h / (p.Hv / p.Hk)) * p.nC * kunit;
+    for (int64_t t = chunks * kC + q; t < p.L; t += 4)
+        if (ok) Elem<T>::store(dv, ((b * p.L + t) * p.Hv + h) * p.V + col, 0.f);
+    for (int64_t c = chunks - 1; c >= 0; --c) {
+        const int64_t t0 = c * kC, bhc = bh * p.nC + c;
+        const uint16_t *kf = p.kf + kat + c * kunit, *ktf = p.ktf + kat + c * kunit, *qtf = p.qtf + kat + c * kunit;
+        const uint16_t *xtf = p.xtf + bhc * 3 * kTri * kFrag, *ptf = p.ptf + bhc * 3 * kTri * kFrag;
+        const float* vec = p.vec + bhc * 3 * kC;
+        float* st = gp.after + bhc * (32 * KS) * VP + col;
+#pragma unroll
+        for (int t = 0; t < 2 * KS; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st[(32 * (t >> 1) + 8 * q + 4 * (t & 1) + r) * VP] = S[t][r];
+        Planes<3> Sp[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = S[2 * s + (j >> 2)][j & 3];
+            split8<3>(x, Sp[s]);
+        }
+        Planes<kN> dO[2];
+        Planes<3> gO[2], Y[2], gE[2];
+        float du[2][8], ga[2][8], be[2][8];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float x[8];
+            load8(vec + 32 * s + 8 * q, ga[s]);
+            load8(vec + 2 * kC + 32 * s + 8 * q, be[s]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t t = t0 + 32 * s + 8 * q + j;
+                x[j] = ok && t < len ? Elem<T>::load(dy, ((b * p.L + t) * p.Hv + h) * p.V + col) : 0.f;
+            }
+            split8<kN>(x, dO[s]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= ga[s][j] * p.scale;
+            split8<3>(x, gO[s]);
+        }
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) {
+            float w[8], x[8];
+            load8(vec + kC + 32 * s2 + 8 * q, w);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f32x4 a = zero4();
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    a = mma<3>(frag<kN>(kf, (2 * s2 + t) * KS + s, 4 * KS, lane), Sp[s], a);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) a[r] *= w[4 * t + r];
+#pragma unroll
+                for (int s = s2; s < 2; ++s)
+                    a = mma<3>(frag<3>(ptf, tri_upper(2 * s2 + t, s), kTri, lane), dO[s], a);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    du[s2][4 * t + r] = a[r];
+                    x[4 * t + r] = be[s2][4 * t + r] * a[r];
+                }
+            }
+            split8<3>(x, Y[s2]);
+        }
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) {
+            float x[8];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f32x4 a = zero4();
+#pragma unroll
+                for (int s = s2; s < 2; ++s)
+                    a = mma<3>(frag<3>(xtf, tri_upper(2 * s2 + t, s), kTri, lane), Y[s], a);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = 4 * t + r, i = 32 * s2 + 8 * q + j;
+                    const float dr = du[s2][j] - a[r], de = be[s2][j] * dr;
+                    gp.dr[(bhc * kC + i) * VP + col] = dr;
+                    if (ok && t0 + i < p.L)
+                        Elem<T>::store(dv, ((b * p.L + t0 + i) * p.Hv + h) * p.V + col, t0 + i < len ? de : 0.f);
+                    x[j] = -ga[s2][j] * de;
+                }
+            }
+            split8<3>(x, gE[s2]);
+        }
+        const float end = vec[kC - 1];
+#pragma unroll
+        for (int t = 0; t < 2 * KS; ++t) {
+            f32x4 a = S[t] * end;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                a = mma<3>(frag<kN>(qtf, 2 * t + s, 4 * KS, lane), gO[s], a);
+                a = mma<3>(frag<kN>(ktf, 2 * t + s, 4 * KS, lane), gE[s], a);
+            }
+            S[t] = a;
+        }
+    }
+    if (gp.dh0) store_state<KS>(gp.dh0 + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
+}
+
+// 8 elements v0 .. v0 + 7 of a row of V elements, zeros behind its end or where !ok
+template <typename T>
+__device__ __forceinline__ void row8(const T* row, int64_t v0, int64_t V, bool ok, bool vec, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = 0.f;
+    if (!ok || v0 >= V) return;
+    if (vec) {
+        if constexpr (sizeof(T) == 2) {
+            const uint4 w = *reinterpret_cast<const uint4*>(row + v0);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(u[j]), x[2 * j + 1] = bf16_hi(u[j]);
+        } else {
+            load8(reinterpret_cast<const float*>(row + v0), x);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (v0 + j < V) x[j] = Elem<T>::load(row, v0 + j);
+}
+
+template <int N>
+__device__ __forceinline__ float plane_sum(const Planes<N>& a, int j) {
+    float x = 0.f;
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) x += static_cast<float>(a.p[n][j]);
+    return x;
+}
+
+__device__ __forceinline__ float sum_quarters(float x) {  // over the four lanes of one column
+    x += __shfl_xor(x, 16, 64);
+    x += __shfl_xor(x, 32, 64);
+    return x;
+}
+
+// A chunk's gradients, one workgroup per key head; wave w owns the 16 steps of
+// tile w as columns of every product (dQ^T, dK^T are K x 16), so the masked
+// 64 x 16 blocks of W1, W2 and their transposes pass from one product's result
+// to the next one's right operand in registers.
+template <typename T, int KS>
+__global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
+    constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut;
+    __shared__ double s_g[kC];
+    __shared__ float s_dg[kC], s_db[kC], s_end[4];
+    const Params& p = gp.f;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4;
+    const int64_t c = blockIdx.x % p.nC, bh = blockIdx.x / p.nC, b = bh / p.Hk, hk = bh % p.Hk;
+    const int64_t t0 = c * kC, group = p.Hv / p.Hk, VP = p.VP;
+    const int64_t len = row_len(p.lengths, b, p.L);
+    const int n = tile_row(wave, lane & 15);  // this lane's step as a column
+    const int64_t tn = t0 + n;
+    T *dq = static_cast<T*>(gp.dq), *dk = static_cast<T*>(gp.dk);
+    T *dg = static_cast<T*>(gp.dg), *db = static_cast<T*>(gp.dbeta);
+    f32x4 dq_all[2 * KS], dk_all[2 * KS];
+#pragma unroll
+    for (int t = 0; t < 2 * KS; ++t) dq_all[t] = dk_all[t] = zero4();
+    const int64_t kunit = static_cast<int64_t>(kN) * 4 * KS * kFrag, kat = (bh * p.nC + c) * kunit;
+    for (int64_t hv = hk * group; hv < (hk + 1) * group; ++hv) {
+        const int64_t gate = (b * p.L + t0 + lane) * p.Hv + hv;
+        if (t0 >= len) {
+            if (wave == 0 && t0 + lane < p.L) {
+                Elem<T>::store(dg, gate, 0.f);
+                Elem<T>::store(db, gate, 0.f);
+            }
+            continue;
+        }
+        const int64_t bhc = (b * p.Hv + hv) * p.nC + c;
+        const float* vec = p.vec + bhc * 3 * kC;
+        float g_raw = 0.f;
+        if (wave == 0) {
+            g_raw = t0 + lane < len ? Elem<T>::load(static_cast<const T*>(p.g), gate) : 0.f;
+            double G = g_raw < kClear ? kClear : g_raw;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_up(G, off, 64);
+                if (lane >= off) G += o;
+            }
+            s_g[lane] = G;
+        }
+        __syncthreads();
+        const float ga_n = vec[n], w_n = vec[kC + n], be_n = vec[2 * kC + n];
+        f32x4 D1[2 * KS], D2[2 * KS], D3[2 * KS], A1[4], A2[4], B1[4], B2[4];
+#pragma unroll
+        for (int t = 0; t < 2 * KS; ++t) D1[t] = D2[t] = D3[t] = zero4();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) A1[t] = A2[t] = B1[t] = B2[t] = zero4();
+        float dbeta = 0.f, bound = 0.f;
+        const T* dyh = static_cast<const T*>(gp.dy) + (b * p.L * p.Hv + hv) * p.V;
+        const float *dr = gp.dr + bhc * kC * VP, *news = p.news + bhc * kC * VP;
+        const float *Sa = p.states + bhc * (32 * KS) * VP, *Sb = gp.after + bhc * (32 * KS) * VP;
+        for (int64_t v0 = 8 * q; v0 < VP; v0 += 32) {
+            float x[8], y[8];
+            Planes<kN> On;
+            Planes<kO> En, Un;
+            row8<T>(dyh + tn * p.Hv * p.V, v0, p.V, tn < len, gp.vec_v, x);
+            split8<kN>(x, On);
+            load8(dr + n * VP + v0, x);
+            load8(news + n * VP + v0, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dbeta += x[j] * y[j];
+                x[j] *= be_n;
+                y[j] *= be_n;
+            }
+            split8<kO>(x, En);
+            split8<kO>(y, Un);
+#pragma unroll
+            for (int t = 0; t < 2 * KS; ++t) {
+                const int64_t at = static_cast<int64_t>(tile_row(t, lane & 15)) * VP + v0;
+                Planes<kO> a, d;
+                load8(Sa + at, x);
+                load8(Sb + at, y);
+                if ((t & 3) == wave)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) bound += x[j] * y[j];
+                split8<kO>(x, a);
+                split8<kO>(y, d);
+                D1[t] = mma<kO>(a, On, D1[t]);
+                D2[t] = mma<kO>(a, En, D2[t]);
+                D3[t] = mma<kO>(d, Un, D3[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int m = tile_row(t, lane & 15);
+                const float be_m = vec[2 * kC + m];
+                if (t / 2 <= wave / 2) {  // rows j not behind this wave's steps
+                    Planes<kO> u;
+                    load8(news + m * VP + v0, x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] *= be_m;
+                    split8<kO>(x, u);
+                    A1[t] = mma<kO>(u, On, A1[t]);
+                    A2[t] = mma<kO>(u, En, A2[t]);
+                }
+                if (t / 2 >= wave / 2) {  // rows i not before them
+                    Planes<kN> o;
+                    Planes<kO> e;
+                    row8<T>(dyh + (t0 + m) * p.Hv * p.V, v0, p.V, t0 + m < len, gp.vec_v, x);
+                    split8<kN>(x, o);
+                    load8(dr + m * VP + v0, x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] *= be_m;
+                    split8<kO>(x, e);
+                    B1[t] = mma<kO>(o, Un, B1[t]);
+                    B2[t] = mma<kO>(e, Un, B2[t]);
+                }
+            }
+        }
+        // decays and masks, then the blocks as right operands: k step s = tiles 2s, 2s + 1
+        Planes<kO> a1[2], a2[2], b1[2], b2[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float xa1[8], xa2[8], xb1[8], xb2[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int t = 2 * s + (j >> 2), m = 32 * s + 8 * q + j;
+                const float up = m <= n ? expf(static_cast<float>(s_g[n] - s_g[m])) : 0.f;
+                const float dn = m >= n ? expf(static_cast<float>(s_g[m] - s_g[n])) : 0.f;
+                xa1[j] = m <= n ? A1[t][j & 3] * up : 0.f;
+                xa2[j] = m < n ? A2[t][j & 3] * up : 0.f;
+                xb1[j] = m >= n ? B1[t][j & 3] * dn * p.scale : 0.f;
+                xb2[j] = m > n ? -B2[t][j & 3] * dn : 0.f;
+            }
+            split8<kO>(xa1, a1[s]);
+            split8<kO>(xa2, a2[s]);
+            split8<kO>(xb1, b1[s]);
+            split8<kO>(xb2, b2[s]);
+        }
+        float dG = 0.f, kover = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2 * KS; ++t) {
+            f32x4 gq = D1[t] * ga_n, row = D2[t] * ga_n, col = D3[t] * w_n;
+            const Planes<kN> kr = frag<kN>(p.kf + kat, wave * KS + (t >> 1), 4 * KS, lane);
+            const Planes<kN> qr = frag<kN>(p.qf + kat, wave * KS + (t >> 1), 4 * KS, lane);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) kover += plane_sum(kr, 4 * (t & 1) + r) * col[r];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Planes<kN> kt = frag<kN>(p.ktf + kat, 2 * t + s, 4 * KS, lane);
+                const Planes<kN> qt = frag<kN>(p.qtf + kat, 2 * t + s, 4 * KS, lane);
+                gq = mma<kO>(kt, a1[s], gq);
+                row = mma<kO>(kt, a2[s], row);
+                col = mma<kO>(qt, b1[s], col);
+                col = mma<kO>(kt, b2[s], col);
+            }
+            gq *= p.scale;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                dG += plane_sum(qr, 4 * (t & 1) + r) * gq[r];
+                dG -= plane_sum(kr, 4 * (t & 1) + r) * (row[r] + col[r]);
+            }
+            dq_all[t] += gq;
+            dk_all[t] += col - row;
+        }
+        dG = sum_quarters(dG);
+        dbeta = sum_quarters(dbeta);
+        if (q == 0) {
+            s_dg[n] = dG;
+            s_db[n] = dbeta;
+        }
+        bound = bound * vec[kC - 1] + kover;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) bound += __shfl_xor(bound, off, 64);
+        if (lane == 0) s_end[wave] = bound;
+        __syncthreads();
+        if (wave == 0) {
+            double x = s_dg[lane];
+            if (lane == 63) x += static_cast<double>(s_end[0]) + s_end[1] + s_end[2] + s_end[3];
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_down(x, off, 64);
+                if (lane + off < 64) x += o;
+            }
+            const bool in = t0 + lane < len;
+            if (t0 + lane < p.L) {
+                Elem<T>::store(dg, gate, in && !(g_raw <= kClear) ? static_cast<float>(x) : 0.f);
+                Elem<T>::store(db, gate, in ? s_db[lane] : 0.f);
+            }
+        }
+        __syncthreads();
+    }
+    if (tn < p.L) {
+        const int64_t at = ((b * p.L + tn) * p.Hk + hk) * p.K;
+#pragma unroll
+        for (int t = 0; t < 2 * KS; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int e = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r;
+                if (e < p.K) {
+                    Elem<T>::store(dq, at + e, tn < len ? dq_all[t][r] : 0.f);
+                    Elem<T>::store(dk, at + e, tn < len ? dk_all[t][r] : 0.f);
+                }
+            }
+    }
+}
+
+}  // namespace delta
+}  // namespace ssm

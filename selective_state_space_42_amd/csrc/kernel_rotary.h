@@ -1,0 +1,117 @@
+// kernel_rotary.h -- rotary positions (include/ssm_rotary.h).
+//
+// One thread turns VEC (half layout: two pieces of VEC elements, i and
+// i + R/2) or VEC / 2 (interleaved: one piece) pairs of one token, for
+// `heads_per` heads of the row, so their sines and cosines are formed once.
+// The angle p inv_freq is an fp64 product (exact for |p| < 2^29), reduced in
+// fp64: fp32 accuracy at any position.  Elements behind R are copied by
+// further items of the same row.  q and k heads are one list of heads.
+#pragma once
+
+#include "device_common.h"
+#include "device_math.h"
+
+namespace ssm {
+namespace rotary {
+
+struct Params {
+    const void *q, *k;
+    const float* inv_freq;
+    const int64_t* positions;
+    void *q_out, *k_out;
+    int64_t tokens, L, Hq, Hk, K, R, offset;
+    int64_t items, turned;   // items of a head: `turned` of them turn, the others copy
+    int64_t groups;          // a row's heads are h, h + groups, h + 2 groups, ...
+    float amplitude, sign;   // sign of the sine
+};
+
+template <typename T, int VEC>
+struct Piece {
+    float x[VEC];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC == 1) {
+            x[0] = Elem<T>::load(p, 0);
+        } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(p);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 2) {
+                    x[2 * j] = bf16_lo(u[j]);
+                    x[2 * j + 1] = bf16_hi(u[j]);
+                } else {
+                    x[j] = __uint_as_float(u[j]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (VEC == 1) {
+            Elem<T>::store(p, 0, x[0]);
+        } else if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                      pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                                      __float_as_uint(x[2]), __float_as_uint(x[3]));
+        }
+    }
+};
+
+// PAIRED: interleaved pairs.  VEC 1 takes one pair (or one copied element) a thread.
+template <typename T, int VEC, bool PAIRED>
+__global__ void __launch_bounds__(256) rotary_kernel(Params p) {
+    constexpr int kPairs = PAIRED && VEC > 1 ? VEC / 2 : VEC;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t per = p.items * p.groups;
+    if (at >= p.tokens * per) return;
+    const int64_t tok = at / per, in = at % per, g = in / p.items, it = in % p.items;
+    const bool turn = it < p.turned;
+    // first element, and the other half's where the halves are apart
+    const int64_t e0 = !turn ? p.R + (it - p.turned) * VEC : PAIRED ? it * 2 * kPairs : it * VEC;
+    const int64_t e1 = e0 + (PAIRED ? (VEC == 1 ? 1 : 0) : p.R / 2);
+    float c[kPairs], s[kPairs];
+    if (turn) {
+        const int64_t pos = (p.positions ? p.positions[tok] : tok % p.L) + p.offset;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            sin_cos_wide(static_cast<double>(pos) * p.inv_freq[it * kPairs + i], &s[i], &c[i]);
+            c[i] *= p.amplitude;
+            s[i] *= p.sign * p.amplitude;
+        }
+    }
+    const int64_t heads = p.Hq + p.Hk;
+    for (int64_t h = g; h < heads; h += p.groups) {
+        const bool is_q = h < p.Hq;
+        const int64_t row = (is_q ? tok * p.Hq + h : tok * p.Hk + h - p.Hq) * p.K;
+        const T* src = static_cast<const T*>(is_q ? p.q : p.k) + row;
+        T* dst = static_cast<T*>(is_q ? p.q_out : p.k_out) + row;
+        Piece<T, VEC> a, b;
+        a.load(src + e0);
+        if (!turn) {
+            a.store(dst + e0);
+            continue;
+        }
+        if constexpr (PAIRED && VEC > 1) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const float u = a.x[2 * i], v = a.x[2 * i + 1];
+                a.x[2 * i] = u * c[i] - v * s[i];
+                a.x[2 * i + 1] = u * s[i] + v * c[i];
+            }
+        } else {
+            b.load(src + e1);
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const float u = a.x[i], v = b.x[i];
+                a.x[i] = u * c[i] - v * s[i];
+                b.x[i] = u * s[i] + v * c[i];
+            }
+            b.store(dst + e1);
+        }
+        a.store(dst + e0);
+    }
+}
+
+}  // namespace rotary
+}  // namespace ssm

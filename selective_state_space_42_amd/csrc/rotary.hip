@@ -1,0 +1,85 @@
+// rotary.hip -- host side of include/ssm_rotary.h: argument checks and launch.
+#include "ssm_rotary.h"
+
+#include "host_common.h"
+#include "kernel_rotary.h"
+
+namespace {
+
+int check_desc(const ssm_rotary_desc_t* d) {
+    if (!d) return SSM_ERR_INVALID_ARGUMENT;
+    if (d->batch < 1 || d->seqlen < 1 || d->qheads < 1 || d->kheads < 0 || d->dhead < 2)
+        return SSM_ERR_INVALID_ARGUMENT;
+    if (d->rotary < 2 || d->rotary > d->dhead || d->rotary % 2) return SSM_ERR_INVALID_ARGUMENT;
+    if (!ssm::finite(d->amplitude)) return SSM_ERR_INVALID_ARGUMENT;
+    if (d->io_dtype != SSM_DTYPE_F32 && d->io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
+    if ((d->interleaved != 0 && d->interleaved != 1) || (d->inverse != 0 && d->inverse != 1))
+        return SSM_ERR_INVALID_ARGUMENT;
+    int64_t heads;
+    if (__builtin_add_overflow(d->qheads, d->kheads, &heads)) return SSM_ERR_INVALID_ARGUMENT;
+    if (!ssm::product_fits({d->batch, d->seqlen, heads, d->dhead}, int64_t(1) << 60)) return SSM_ERR_INVALID_ARGUMENT;
+    if (d->dhead > 65536) return SSM_ERR_UNSUPPORTED;
+    return SSM_OK;
+}
+
+template <typename T>
+int launch(const ssm_rotary_desc_t* d, ssm::rotary::Params& p, hipStream_t s) {
+    constexpr int kVec = 16 / sizeof(T);
+    const int64_t half = p.R / 2;
+    // 16-byte pieces, when every row and every piece of it starts on one
+    const bool vec = p.K % kVec == 0 && (d->interleaved ? p.R : half) % kVec == 0 && ssm::aligned(p.q, 16) &&
+                     ssm::aligned(p.q_out, 16) && (!p.k || (ssm::aligned(p.k, 16) && ssm::aligned(p.k_out, 16)));
+    const int64_t width = vec ? kVec : 1;
+    p.turned = vec ? (d->interleaved ? p.R : half) / kVec : half;
+    const bool copies = p.q != p.q_out || (p.k && p.k != p.k_out);
+    p.items = p.turned + (copies ? (p.K - p.R) / width : 0);
+    // one head a thread, unless that is far more threads than fill the GPU: then
+    // the heads of a row share their angles
+    const int64_t heads = p.Hq + p.Hk, rows = p.tokens * p.items;
+    p.groups = heads;
+    while (p.groups > 1 && rows * p.groups > (int64_t(1) << 19)) p.groups = (p.groups + 1) / 2;
+    int64_t blocks;
+    if (__builtin_mul_overflow(rows, p.groups, &blocks)) return SSM_ERR_UNSUPPORTED;
+    blocks = (blocks + 255) / 256;
+    if (blocks > INT32_MAX) return SSM_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+    using namespace ssm::rotary;
+    if (vec && d->interleaved)
+        hipLaunchKernelGGL((rotary_kernel<T, kVec, true>), grid, block, 0, s, p);
+    else if (vec)
+        hipLaunchKernelGGL((rotary_kernel<T, kVec, false>), grid, block, 0, s, p);
+    else if (d->interleaved)
+        hipLaunchKernelGGL((rotary_kernel<T, 1, true>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((rotary_kernel<T, 1, false>), grid, block, 0, s, p);
+    return ssm::launch_status();
+}
+
+}  // namespace
+
+extern "C" int ssm_rotary(const ssm_rotary_desc_t* d, const void* q, const void* k, const float* inv_freq,
+                          const int64_t* positions, void* q_out, void* k_out, void* stream) {
+    const int st = check_desc(d);
+    if (st != SSM_OK) return st;
+    if (!q || !q_out || !inv_freq) return SSM_ERR_INVALID_ARGUMENT;
+    if ((k != nullptr) != (d->kheads > 0) || (k_out != nullptr) != (d->kheads > 0)) return SSM_ERR_INVALID_ARGUMENT;
+    const size_t es = d->io_dtype == SSM_DTYPE_F32 ? 4 : 2;
+    for (const void* x : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
+        if (x && !ssm::aligned(x, es)) return SSM_ERR_INVALID_ARGUMENT;
+    if (!ssm::aligned(inv_freq, 4) || (positions && !ssm::aligned(positions, 8))) return SSM_ERR_INVALID_ARGUMENT;
+    // each output is its input itself, or apart from every input and output
+    const uint64_t rows = static_cast<uint64_t>(d->batch) * d->seqlen * d->dhead * es;
+    const ssm::Range rq{q, rows * d->qheads}, rk{k, rows * d->kheads}, oq{q_out, rows * d->qheads},
+        ok{k_out, rows * d->kheads};
+    if ((q != q_out && overlap(oq, rq)) || (k && k != k_out && overlap(ok, rk))) return SSM_ERR_INVALID_ARGUMENT;
+    if (k && (overlap(oq, ok) || overlap(oq, rk) || overlap(ok, rq))) return SSM_ERR_INVALID_ARGUMENT;
+
+    ssm::rotary::Params p{};
+    p.q = q; p.k = k; p.inv_freq = inv_freq; p.positions = positions; p.q_out = q_out; p.k_out = k_out;
+    p.tokens = d->batch * d->seqlen; p.L = d->seqlen; p.Hq = d->qheads; p.Hk = d->kheads;
+    p.K = d->dhead; p.R = d->rotary; p.offset = d->offset;
+    p.amplitude = d->amplitude;
+    p.sign = d->inverse ? -1.f : 1.f;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return d->io_dtype == SSM_DTYPE_F32 ? launch<float>(d, p, s) : launch<uint16_t>(d, p, s);
+}

@@ -13,6 +13,7 @@
 
 #include "ssm_scan.h"
 #include "device_common.h"
+#include "host_common.h"
 #include "kernel_sequential.h"
 #include "kernel_sweep.h"
 #include "kernel_chunked.h"
@@ -28,8 +29,16 @@
 static __device__ __align__(256) unsigned char scratch[SSM_SCAN_NOALLOC_SCRATCH_BYTES];
 
 namespace {
-
 thread_local int g_last_hip_error = 0;
+}  // namespace
+
+int ssm::hip_status(hipError_t e) {
+    if (e == hipSuccess) return SSM_OK;
+    g_last_hip_error = static_cast<int>(e);
+    return SSM_ERR_HIP;
+}
+
+namespace {
 
 // Device address of `scratch` on each GPU, looked up once per device with
 // that device current.
@@ -63,13 +72,8 @@ void* scratch_for_current_device() {
     return g_scratch_ptr[dev];
 }
 
-int hip_status(hipError_t e) {
-    if (e == hipSuccess) return SSM_OK;
-    g_last_hip_error = static_cast<int>(e);
-    return SSM_ERR_HIP;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using ssm::aligned;
+using ssm::hip_status;
 
 int next_pow2(int64_t v) {
     int r = 1;

@@ -7,7 +7,9 @@ these functions raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -45,6 +47,23 @@ class MimoDesc(ctypes.Structure):
         ("dstate", ctypes.c_int64), ("rank", ctypes.c_int64), ("chunk", ctypes.c_int64),
         ("io_dtype", ctypes.c_int32), ("disc", ctypes.c_int32), ("is_complex", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class DeltaDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("kheads", ctypes.c_int64),
+        ("vheads", ctypes.c_int64), ("dkey", ctypes.c_int64), ("dvalue", ctypes.c_int64),
+        ("scale", ctypes.c_float), ("io_dtype", ctypes.c_int32),
+    ]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("qheads", ctypes.c_int64),
+        ("kheads", ctypes.c_int64), ("dhead", ctypes.c_int64), ("rotary", ctypes.c_int64),
+        ("offset", ctypes.c_int64), ("amplitude", ctypes.c_float), ("interleaved", ctypes.c_int32),
+        ("inverse", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
     ]
 
 
@@ -94,6 +113,17 @@ def _lib():
     lib.ssm_mimo_step.restype = ctypes.c_int
     lib.ssm_mimo_workspace_bytes.argtypes = [ctypes.POINTER(MimoDesc)]
     lib.ssm_mimo_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssm_delta_fwd.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 10 + [ctypes.c_size_t, vp]
+    lib.ssm_delta_fwd.restype = ctypes.c_int
+    lib.ssm_delta_step.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 8
+    lib.ssm_delta_step.restype = ctypes.c_int
+    lib.ssm_delta_bwd.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 16 + [ctypes.c_size_t, vp]
+    lib.ssm_delta_bwd.restype = ctypes.c_int
+    for f in (lib.ssm_delta_workspace_bytes, lib.ssm_delta_bwd_workspace_bytes):
+        f.argtypes = [ctypes.POINTER(DeltaDesc)]
+        f.restype = ctypes.c_size_t
+    lib.ssm_rotary.argtypes = [ctypes.POINTER(RotaryDesc)] + [vp] * 7
+    lib.ssm_rotary.restype = ctypes.c_int
     lib.ssm_scan_algo.argtypes = [ctypes.POINTER(ScanDesc)]
     lib.ssm_scan_algo.restype = ctypes.c_int
     lib.ssm_scan_workspace_bytes.argtypes = [ctypes.POINTER(ScanDesc)]
@@ -560,3 +590,227 @@ def ssm_mimo_step(u, delta, A, B, C, D=None, theta=None, lam=None, *, h, u_prev=
     if st != 0:
         raise ScanError(st, "ssm_mimo_step")
     return y
+
+
+def _on(device, stream):
+    """A context in which `device` is the current one and tensors allocated
+    for the call belong to `stream` (a raw hipStream_t, or None), so that the
+    allocator does not hand a workspace on while that stream still uses it."""
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
+    if device.index is not None and device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def make_delta_desc(batch, seqlen, kheads, vheads, dkey, dvalue, io_dtype, scale=None) -> DeltaDesc:
+    return DeltaDesc(int(batch), int(seqlen), int(kheads), int(vheads), int(dkey), int(dvalue),
+                     float(scale if scale is not None else max(int(dkey), 1) ** -0.5),
+                     int(SSM_DTYPE.get(io_dtype, io_dtype)))
+
+
+def ssm_delta_workspace_bytes(desc: DeltaDesc) -> int:
+    return int(_lib().ssm_delta_workspace_bytes(ctypes.byref(desc)))
+
+
+def ssm_delta_bwd_workspace_bytes(desc: DeltaDesc) -> int:
+    return int(_lib().ssm_delta_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def _delta_dims(where: str, q, v):
+    B, L, Hk, K = _dims(where, q, 4, "q")
+    Hv, V = _dims(where, v, 4, "v")[2:]
+    if Hk < 1 or Hv % Hk:
+        raise ValueError(f"{where}: the {Hv} heads of v are not a multiple of the {Hk} heads of q")
+    return B, L, Hk, Hv, K, V
+
+
+def ssm_delta_fwd(q, k, v, g, beta, h0=None, *, scale=None, lengths=None, y=None, h_last=None,
+                  want_h_last: bool = True, workspace=None, stream=None):
+    """The gated delta rule over whole sequences; returns (y, h_last).
+
+    Per value head, with a state S (V x K): u_t = beta_t (v_t - e^{g_t} S_{t-1} k_t),
+    S_t = e^{g_t} S_{t-1} + u_t k_t^T, y_t = scale S_t q_t (include/ssm_delta.h).
+
+    q, k (B,L,Hk,K); v (B,L,Hv,V) with Hv a multiple of Hk; g, beta (B,L,Hv);
+    h0 and h_last (B,Hv,V,K) fp32; lengths (B,) int32, the steps of each row
+    that count.  scale defaults to K^-1/2.  Rows of y behind a row's length
+    are left as they were (zeros when y is allocated here).
+    """
+    where = "ssm_delta_fwd"
+    B, L, Hk, Hv, K, V = _delta_dims(where, q, v)
+    state, f32 = (B, Hv, V, K), torch.float32
+    _check(where, q.dtype, [
+        ("q", q, (B, L, Hk, K), None), ("k", k, (B, L, Hk, K), None), ("v", v, (B, L, Hv, V), None),
+        ("g", g, (B, L, Hv), None), ("beta", beta, (B, L, Hv), None), ("h0", h0, state, f32),
+        ("lengths", lengths, (B,), torch.int32), ("y", y, (B, L, Hv, V), None), ("h_last", h_last, state, f32)])
+    _check_workspace(where, workspace, q.device)
+    desc = make_delta_desc(B, L, Hk, Hv, K, V, q.dtype, scale)
+    with _on(q.device, stream):
+        if y is None:
+            y = torch.empty_like(v) if lengths is None else torch.zeros_like(v)
+        if h_last is None and want_h_last:
+            h_last = torch.empty(state, dtype=f32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(max(ssm_delta_workspace_bytes(desc), 1), dtype=torch.uint8, device=q.device)
+        if stream is None:
+            stream = torch.cuda.current_stream(q.device).cuda_stream
+        st = _lib().ssm_delta_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
+                                  _ptr(lengths), _ptr(y), _ptr(h_last), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), ctypes.c_void_p(stream))
+    if st != 0:
+        raise ScanError(st, where)
+    return y, h_last
+
+
+def ssm_delta_step(q, k, v, g, beta, *, h, scale=None, y=None, stream=None):
+    """One decode step of the gated delta rule, updating h in place; returns y.
+
+    q, k (B,Hk,K); v, y (B,Hv,V); g, beta (B,Hv); h (B,Hv,V,K) fp32.
+    """
+    where = "ssm_delta_step"
+    B, Hk, K = _dims(where, q, 3, "q")
+    Hv, V = _dims(where, v, 3, "v")[1:]
+    if Hk < 1 or Hv % Hk:
+        raise ValueError(f"{where}: the {Hv} heads of v are not a multiple of the {Hk} heads of q")
+    if h is None:
+        raise ValueError(f"{where}: h is required")
+    _check(where, q.dtype, [
+        ("q", q, (B, Hk, K), None), ("k", k, (B, Hk, K), None), ("v", v, (B, Hv, V), None), ("g", g, (B, Hv), None),
+        ("beta", beta, (B, Hv), None), ("h", h, (B, Hv, V, K), torch.float32), ("y", y, (B, Hv, V), None)])
+    desc = make_delta_desc(B, 1, Hk, Hv, K, V, q.dtype, scale)
+    with _on(q.device, stream):
+        if y is None:
+            y = torch.empty_like(v)
+        if stream is None:
+            stream = torch.cuda.current_stream(q.device).cuda_stream
+        st = _lib().ssm_delta_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h),
+                                   _ptr(y), ctypes.c_void_p(stream))
+    if st != 0:
+        raise ScanError(st, where)
+    return y
+
+
+def ssm_delta_bwd(q, k, v, g, beta, h0=None, *, dy, dh_last=None, scale=None, lengths=None, want_dh0: bool = False,
+                  workspace=None, stream=None) -> dict:
+    """Gradients of sum(dy * y) + <dh_last, h_last> of ssm_delta_fwd; returns a
+    dict of dq, dk, dv, dg, dbeta (the inputs' shapes and dtype) and dh0 (fp32;
+    None unless want_dh0).  Rows behind a row's length get zeros."""
+    where = "ssm_delta_bwd"
+    B, L, Hk, Hv, K, V = _delta_dims(where, q, v)
+    state, f32 = (B, Hv, V, K), torch.float32
+    if dy is None:
+        raise ValueError(f"{where}: dy is required")
+    _check(where, q.dtype, [
+        ("q", q, (B, L, Hk, K), None), ("k", k, (B, L, Hk, K), None), ("v", v, (B, L, Hv, V), None),
+        ("g", g, (B, L, Hv), None), ("beta", beta, (B, L, Hv), None), ("h0", h0, state, f32),
+        ("lengths", lengths, (B,), torch.int32), ("dy", dy, (B, L, Hv, V), None), ("dh_last", dh_last, state, f32)])
+    _check_workspace(where, workspace, q.device)
+    desc = make_delta_desc(B, L, Hk, Hv, K, V, q.dtype, scale)
+    with _on(q.device, stream):
+        out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), dg=torch.empty_like(g),
+                   dbeta=torch.empty_like(beta),
+                   dh0=torch.empty(state, dtype=f32, device=q.device) if want_dh0 else None)
+        if workspace is None:
+            workspace = torch.empty(max(ssm_delta_bwd_workspace_bytes(desc), 1), dtype=torch.uint8, device=q.device)
+        if stream is None:
+            stream = torch.cuda.current_stream(q.device).cuda_stream
+        st = _lib().ssm_delta_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
+                                  _ptr(lengths), _ptr(dy), _ptr(dh_last),
+                                  *(_ptr(out[n]) for n in ("dq", "dk", "dv", "dg", "dbeta", "dh0")),
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                  ctypes.c_void_p(stream))
+    if st != 0:
+        raise ScanError(st, where)
+    return out
+
+
+ROTARY_SCALING = ("none", "linear", "base", "bands")
+
+
+def ssm_rotary_freqs(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                     trained_len: int = 4096, fast: float = 32.0, slow: float = 1.0, device=None):
+    """(inv_freq, amplitude) for ssm_rotary_fwd: the R / 2 angles per position
+    base^(-2i/R) and the factor of the turned elements, scaled for contexts
+    `factor` times longer than the trained ones:
+
+    none    as they are
+    linear  every angle divided by factor (positions interpolated)
+    base    a larger base, base factor^(R/(R-2)): the slowest pair is divided by
+            factor, the fastest stays
+    bands   pairs that turn more than `fast` times in trained_len positions stay,
+            pairs that turn less than `slow` times are divided by factor, a
+            linear ramp between; amplitude 0.1 ln(factor) + 1
+    """
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("ssm_rotary_freqs: rotary_dim must be even and positive")
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"ssm_rotary_freqs: scaling must be one of {ROTARY_SCALING}, got {scaling!r}")
+    if not (base > 0 and factor >= 1 and trained_len > 0 and fast > slow):
+        raise ValueError("ssm_rotary_freqs: base and trained_len must be positive, factor at least 1, fast above slow")
+    if scaling == "base":
+        base = base * factor ** (rotary_dim / max(rotary_dim - 2, 1))
+    f = base ** -(torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        keep = ((trained_len * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    return f.float().to(device or "cpu"), amplitude
+
+
+def _rotary(where, q, k, inv_freq, positions, offset, interleaved, inverse, amplitude, q_out, k_out, stream):
+    B, L, Hq, K = _dims(where, q, 4, "q")
+    Hk = 0 if k is None else _dims(where, k, 4, "k")[2]
+    if k is not None and Hk < 1:
+        raise ValueError(f"{where}: k has no heads (pass None)")
+    if k is None and k_out is not None:
+        raise ValueError(f"{where}: k_out is given without k")
+    half = _dims(where, inv_freq, 1, "inv_freq")[0]
+    _check(where, q.dtype, [
+        ("q", q, (B, L, Hq, K), None), ("k", k, (B, L, Hk, K), None), ("inv_freq", inv_freq, (half,), torch.float32),
+        ("positions", positions, (B, L), torch.int64), ("q_out", q_out, (B, L, Hq, K), None),
+        ("k_out", k_out, (B, L, Hk, K), None)])
+    if 2 * half > K:
+        raise ValueError(f"{where}: inv_freq has {half} angles, a head of {K} has {K // 2} pairs")
+    desc = RotaryDesc(B, L, Hq, Hk, K, 2 * half, int(offset), float(amplitude), int(bool(interleaved)), int(inverse),
+                      SSM_DTYPE[q.dtype])
+    with _on(q.device, stream):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k)
+        if stream is None:
+            stream = torch.cuda.current_stream(q.device).cuda_stream
+        st = _lib().ssm_rotary(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(inv_freq), _ptr(positions), _ptr(q_out),
+                               _ptr(k_out), ctypes.c_void_p(stream))
+    if st != 0:
+        raise ScanError(st, where)
+    return q_out, k_out
+
+
+def ssm_rotary_fwd(q, k, inv_freq, positions=None, *, offset: int = 0, interleaved: bool = False,
+                   amplitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions; returns (q_out, k_out).
+
+    Each pair (a, b) of a head's first R = 2 len(inv_freq) elements becomes
+    amplitude (a cos t - b sin t, a sin t + b cos t), t = position * inv_freq[i]
+    (include/ssm_rotary.h); the other elements are copied.  Pairs are (i, i + R/2), or
+    (2i, 2i + 1) when interleaved.
+
+    q (B,L,Hq,K); k (B,L,Hk,K) or None; inv_freq (R/2,) fp32 (ssm_rotary_freqs);
+    positions (B,L) int64, 0 .. L-1 when None; offset is added to them.
+    q_out and k_out may be q and k themselves.
+    """
+    return _rotary("ssm_rotary_fwd", q, k, inv_freq, positions, offset, interleaved, 0, amplitude, q_out, k_out,
+                   stream)
+
+
+def ssm_rotary_bwd(dq, dk, inv_freq, positions=None, *, offset: int = 0, interleaved: bool = False,
+                   amplitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Gradients of ssm_rotary_fwd's inputs from those of its outputs (the turn
+    by the angle -t); arguments and layouts as there."""
+    return _rotary("ssm_rotary_bwd", dq, dk, inv_freq, positions, offset, interleaved, 1, amplitude, q_out, k_out,
+                   stream)

@@ -1,0 +1,224 @@
+"""Refusals of the delta rule's and the rotary entry points, without a GPU:
+the C ABI with fake pointers that are never dereferenced, the Python binding
+with the library call replaced by a trap; the 64-bit reference's gradients
+against differences; the frequency helper."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+from delta_util import make, reference, reference_grads, wide
+from selective_state_space_42_amd import scan
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, INVALID, UNSUPPORTED, WS_SMALL = 0, 1, 2, 3
+P = 0x10000
+
+
+def test_library_exports_every_declared_symbol():
+    names = set()
+    for h in ("ssm_delta.h", "ssm_rotary.h"):
+        names |= set(re.findall(r"\b(ssm_(?:delta|rotary)\w*)\s*\(", open(os.path.join(ROOT, "include", h)).read()))
+    assert names == {"ssm_delta_fwd", "ssm_delta_step", "ssm_delta_bwd", "ssm_delta_workspace_bytes",
+                     "ssm_delta_bwd_workspace_bytes", "ssm_rotary"}
+    for n in names:
+        assert hasattr(scan._lib(), n), n
+
+
+def ddesc(B=2, L=100, Hk=2, Hv=4, K=64, V=64, dtype=0, scale=1.0):
+    return scan.make_delta_desc(B, L, Hk, Hv, K, V, dtype, scale)
+
+
+def vp(args):
+    return [ctypes.c_void_p(a) if a else None for a in args]
+
+
+def call_fwd(d, q=P, k=P, v=P, g=P, beta=P, h0=0, lengths=0, y=P, h=0, ws=P, ws_bytes=1 << 50):
+    return scan._lib().ssm_delta_fwd(None if d is None else ctypes.byref(d),
+                                     *vp([q, k, v, g, beta, h0, lengths, y, h, ws]), ws_bytes, None)
+
+
+def call_step(d, q=P, k=P, v=P, g=P, beta=P, h=P, y=P):
+    return scan._lib().ssm_delta_step(None if d is None else ctypes.byref(d), *vp([q, k, v, g, beta, h, y]), None)
+
+
+BWD = ("q", "k", "v", "g", "beta", "h0", "lengths", "dy", "dh_last", "dq", "dk", "dv", "dg", "dbeta", "dh0", "ws")
+OPTIONAL = ("h0", "lengths", "dh_last", "dh0")
+
+
+def call_bwd(d, ws_bytes=1 << 50, **kw):
+    args = [kw.get(n, 0 if n in OPTIONAL else P) for n in BWD]
+    return scan._lib().ssm_delta_bwd(None if d is None else ctypes.byref(d), *vp(args), ws_bytes, None)
+
+
+@pytest.mark.parametrize("call,L", [(call_fwd, 100), (call_step, 1), (call_bwd, 100)])
+def test_delta_descriptor_rules(call, L):
+    assert call(None) == INVALID
+    for kw in [dict(B=0), dict(L=0), dict(L=-1), dict(Hk=0), dict(Hv=0), dict(K=0), dict(V=0), dict(Hk=3),
+               dict(scale=math.inf), dict(scale=math.nan)]:
+        assert call(ddesc(**{"L": L, **kw})) == INVALID, kw
+    for kw in [dict(K=129), dict(V=1025), dict(dtype=2)]:
+        assert call(ddesc(**{"L": L, **kw})) == UNSUPPORTED, kw
+    assert call(ddesc(B=1 << 30, L=1 << 30)) == INVALID
+    assert call(ddesc(B=1 << 24, Hk=1 << 10, Hv=1 << 10, L=1)) == INVALID
+
+
+def test_delta_pointer_rules():
+    for n in ("q", "k", "v", "g", "beta", "y"):
+        assert call_fwd(ddesc(), **{n: 0}) == INVALID, n
+        assert call_fwd(ddesc(), **{n: P + 2}) == INVALID, n
+        assert call_fwd(ddesc(dtype=1), **{n: P + 1}) == INVALID, n
+    for n in ("h0", "lengths", "h"):
+        assert call_fwd(ddesc(), **{n: P + 2}) == INVALID, n
+    assert call_fwd(ddesc(), h0=P, h=P) == INVALID
+    for n in ("q", "k", "v", "g", "beta", "h", "y"):
+        assert call_step(ddesc(L=1), **{n: 0}) == INVALID, n
+        assert call_step(ddesc(L=1), **{n: P + 2}) == INVALID, n
+    assert call_step(ddesc(L=2)) == INVALID
+    for n in BWD[:-1]:
+        if n not in OPTIONAL:
+            assert call_bwd(ddesc(), **{n: 0}) == INVALID, n
+        assert call_bwd(ddesc(), **{n: P + 2}) == INVALID, n
+
+
+def test_delta_workspace_rules():
+    lib = scan._lib()
+    for call, size in ((call_fwd, lib.ssm_delta_workspace_bytes), (call_bwd, lib.ssm_delta_bwd_workspace_bytes)):
+        need = size(ctypes.byref(ddesc()))
+        assert need > 0 and need % 256 == 0
+        assert call(ddesc(), ws=0) == WS_SMALL
+        assert call(ddesc(), ws_bytes=need - 1) == WS_SMALL
+        assert call(ddesc(), ws=P + 64, ws_bytes=need) == INVALID
+        assert size(ctypes.byref(ddesc(K=129))) == 0 and size(None) == 0
+        # 64 steps and 65 differ by one chunk
+        a, b = (size(ctypes.byref(ddesc(L=n))) for n in (64, 128))
+        assert b == 2 * a and size(ctypes.byref(ddesc(L=65))) == b
+
+
+def rdesc(B=2, L=10, Hq=4, Hk=2, K=64, R=64, offset=0, amplitude=1.0, interleaved=0, inverse=0, dtype=0):
+    return scan.RotaryDesc(B, L, Hq, Hk, K, R, offset, amplitude, interleaved, inverse, dtype)
+
+
+Q, KK, QO, KO = P, P + (1 << 20), P + (2 << 20), P + (3 << 20)
+
+
+def call_rotary(d, q=Q, k=KK, inv=P, pos=0, q_out=QO, k_out=KO):
+    return scan._lib().ssm_rotary(None if d is None else ctypes.byref(d), *vp([q, k, inv, pos, q_out, k_out]), None)
+
+
+def test_rotary_rules():
+    assert call_rotary(None) == INVALID
+    for kw in [dict(B=0), dict(L=0), dict(Hq=0), dict(Hk=-1), dict(K=1), dict(R=0), dict(R=65), dict(R=63),
+               dict(R=66), dict(amplitude=math.inf), dict(interleaved=2), dict(inverse=-1), dict(B=1 << 40, L=1 << 40),
+               dict(Hq=(1 << 63) - 1, Hk=1)]:
+        assert call_rotary(rdesc(**kw)) == INVALID, kw
+    assert call_rotary(rdesc(dtype=3)) == UNSUPPORTED
+    assert call_rotary(rdesc(K=65538)) == UNSUPPORTED
+    for n in ("q", "k", "inv", "q_out", "k_out"):
+        assert call_rotary(rdesc(), **{n: 0}) == INVALID, n
+        assert call_rotary(rdesc(), **{n: P + 2}) == INVALID, n
+    assert call_rotary(rdesc(), pos=P + 4) == INVALID
+    assert call_rotary(rdesc(Hk=0)) == INVALID                      # k given without heads
+    assert call_rotary(rdesc(), q_out=Q + 256) == INVALID            # overlapping, not the input itself
+    assert call_rotary(rdesc(), k_out=QO) == INVALID
+    assert call_rotary(rdesc(), q_out=KK) == INVALID
+    assert call_rotary(rdesc(), k_out=Q) == INVALID
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    def trap():
+        raise AssertionError("the library was called")
+    monkeypatch.setattr(scan, "_lib", trap)
+
+
+def dargs(B=2, L=5, Hk=2, Hv=4, K=8, V=6, dtype=torch.bfloat16):
+    z = torch.zeros
+    return dict(q=z(B, L, Hk, K, dtype=dtype), k=z(B, L, Hk, K, dtype=dtype), v=z(B, L, Hv, V, dtype=dtype),
+                g=z(B, L, Hv, dtype=dtype), beta=z(B, L, Hv, dtype=dtype))
+
+
+def test_delta_binding_checks(no_library):
+    a = dargs()
+    with pytest.raises(ValueError, match="GPU"):
+        scan.ssm_delta_fwd(**a)
+    with pytest.raises(ValueError, match="multiple"):
+        scan.ssm_delta_fwd(**{**a, "v": torch.zeros(2, 5, 3, 6, dtype=torch.bfloat16)})
+    for name in a:
+        with pytest.raises(ValueError, match="dtype|float32 or bfloat16"):
+            scan.ssm_delta_fwd(**{**a, name: a[name].half()})
+        wide_t = torch.zeros(a[name].shape[:-1] + (2 * a[name].shape[-1],), dtype=a[name].dtype)[..., ::2]
+        with pytest.raises(ValueError, match="contiguous"):
+            scan.ssm_delta_fwd(**{**a, name: wide_t})
+    with pytest.raises(ValueError, match="h0"):
+        scan.ssm_delta_fwd(**a, h0=torch.zeros(2, 4, 8, 6))
+    with pytest.raises(ValueError, match="lengths"):
+        scan.ssm_delta_fwd(**a, lengths=torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="y has"):
+        scan.ssm_delta_fwd(**a, y=torch.zeros(2, 5, 4, 6))
+    with pytest.raises(ValueError, match="dy"):
+        scan.ssm_delta_bwd(**a, dy=None)
+    with pytest.raises(ValueError, match="dy"):
+        scan.ssm_delta_bwd(**a, dy=a["q"])
+    row = {n: t[:, 0].contiguous() for n, t in a.items()}
+    with pytest.raises(ValueError, match="h is required"):
+        scan.ssm_delta_step(**row, h=None)
+    with pytest.raises(ValueError, match="h has"):
+        scan.ssm_delta_step(**row, h=torch.zeros(2, 4, 8, 6))
+    with pytest.raises(ValueError, match="GPU"):
+        scan.ssm_delta_step(**row, h=torch.zeros(2, 4, 6, 8))
+
+
+def test_rotary_binding_checks(no_library):
+    q, k, inv = torch.zeros(2, 5, 4, 8), torch.zeros(2, 5, 2, 8), torch.zeros(4)
+    with pytest.raises(ValueError, match="GPU"):
+        scan.ssm_rotary_fwd(q, k, inv)
+    for bad in (dict(k=torch.zeros(2, 4, 2, 8)), dict(inv_freq=inv.double()),
+                dict(positions=torch.zeros(2, 5, dtype=torch.int32)), dict(positions=torch.zeros(5, dtype=torch.int64)),
+                dict(q_out=torch.zeros(2, 5, 4, 9)), dict(k=None, k_out=k), dict(k=torch.zeros(2, 5, 0, 8)),
+                dict(q=q.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            scan.ssm_rotary_fwd(**{"q": q, "k": k, "inv_freq": inv, **bad})
+
+
+def test_frequencies():
+    inv, amp = scan.ssm_rotary_freqs(8, base=10000.0)
+    assert amp == 1.0 and torch.allclose(inv, torch.tensor([1.0, 0.1, 0.01, 0.001]), rtol=1e-6)
+    lin, _ = scan.ssm_rotary_freqs(8, scaling="linear", factor=4.0)
+    assert torch.allclose(lin, inv / 4, rtol=1e-6)
+    based, _ = scan.ssm_rotary_freqs(8, scaling="base", factor=4.0)
+    assert torch.allclose(based[0], inv[0]) and torch.allclose(based[-1], inv[-1] / 4, rtol=1e-6)
+    bands, amp = scan.ssm_rotary_freqs(8, scaling="bands", factor=4.0, trained_len=1000)
+    # 1000 positions are 159, 15.9, 1.59 and 0.159 turns: kept, on the ramp twice, divided
+    assert bands[0] == inv[0] and torch.allclose(bands[-1], inv[-1] / 4, rtol=1e-6)
+    assert inv[1] / 4 < bands[1] < inv[1] and inv[2] / 4 < bands[2] < inv[2]
+    assert abs(amp - (0.1 * math.log(4.0) + 1)) < 1e-12
+    for bad in (dict(rotary_dim=7), dict(rotary_dim=0), dict(rotary_dim=8, scaling="other"),
+                dict(rotary_dim=8, factor=0.5), dict(rotary_dim=8, base=0.0)):
+        with pytest.raises(ValueError):
+            scan.ssm_rotary_freqs(**bad)
+
+
+def test_reference_gradients_against_differences():
+    """Central differences in 64 bits: error h^2 |f'''| plus 2^-53 |f| / h, below 1e-7 at h = 1e-5."""
+    x = make(1, 9, 1, 2, 5, 4, torch.float32, seed=1)
+    lengths = torch.tensor([7])
+    g = torch.Generator().manual_seed(2)
+    dy = torch.randn(x["v"].shape, generator=g, dtype=torch.float64)
+    dh = torch.randn(x["h0"].shape, generator=g, dtype=torch.float64)
+    grads = reference_grads(x, dy, dh, lengths=lengths)
+
+    def loss(w):
+        y, h = reference(**w, lengths=lengths)
+        return float((y * dy).sum() + (h * dh).sum())
+
+    for n in ("q", "k", "v", "g", "beta", "h0"):
+        way = torch.randn(x[n].shape, generator=g, dtype=torch.float64)
+        up, down = wide(x), wide(x)
+        up[n] = up[n] + 1e-5 * way
+        down[n] = down[n] - 1e-5 * way
+        slope = (loss(up) - loss(down)) / 2e-5
+        assert abs(slope - float((grads["d" + n] * way).sum())) <= 1e-6 * max(1.0, abs(slope)), n
