@@ -26,7 +26,7 @@ typedef struct {
     int64_t batch;     /* B >= 1 */
     int64_t seqlen;    /* L >= 1 (1 for ssm_delta_step) */
     int64_t kheads;    /* Hk >= 1, heads of q and k */
-    int64_t vheads;    /* Hv, a multiple of Hk: heads of v, g, beta and y */
+    int64_t vheads;    /* Hv, a multiple of Hk, at most 4096: heads of v, g, beta and y */
     int64_t dkey;      /* K, 1 <= K <= 128 */
     int64_t dvalue;    /* V, 1 <= V <= 1024 */
     float scale;       /* of the output; finite */

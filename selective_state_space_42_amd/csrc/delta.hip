@@ -18,7 +18,8 @@ int check_desc(const ssm_delta_desc_t* d) {
         return SSM_ERR_INVALID_ARGUMENT;
     if (d->vheads % d->kheads || !ssm::finite(d->scale)) return SSM_ERR_INVALID_ARGUMENT;
     if (d->io_dtype != SSM_DTYPE_F32 && d->io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
-    if (d->dkey > 128 || d->dvalue > 1024) return SSM_ERR_UNSUPPORTED;
+    // a chunk's rows are reached by 32-bit offsets: 64 rows of at most 4096 x 1024 elements
+    if (d->dkey > 128 || d->dvalue > 1024 || d->vheads > 4096) return SSM_ERR_UNSUPPORTED;
     if (!ssm::product_fits({d->batch, d->seqlen, d->vheads, 1024}, kMaxElements) ||
         !ssm::product_fits({d->batch, (d->seqlen + kC - 1) / kC, d->vheads, (d->dvalue + 15) / 16}, INT32_MAX))
         return SSM_ERR_INVALID_ARGUMENT;
@@ -26,31 +27,32 @@ int check_desc(const ssm_delta_desc_t* d) {
 }
 
 struct Layout {
-    size_t kf, ktf, qf, qtf, xf, xtf, pf, ptf, vec, states, news, after, dr, total;
+    size_t kr, qr, blk, states, news, after, dr, total;
 };
+
+int64_t key_steps(const ssm_delta_desc_t* d) { return (d->dkey + 31) / 32; }
+
+// keys and queries that are copied as they are: bf16 rows of whole 16-byte pieces
+bool plain_rows(const ssm_delta_desc_t* d, const void* q, const void* k) {
+    return d->io_dtype == SSM_DTYPE_BF16 && d->dkey % 8 == 0 && ssm::aligned(q, 16) && ssm::aligned(k, 16);
+}
 
 Layout layout(const ssm_delta_desc_t* d, bool bwd) {
     Layout o{};
-    const size_t nC = (d->seqlen + kC - 1) / kC, in = d->io_dtype == SSM_DTYPE_F32 ? 3 : 1;
+    const bool f32 = d->io_dtype == SSM_DTYPE_F32;
+    const size_t nC = (d->seqlen + kC - 1) / kC;
     const size_t kc = d->batch * d->kheads * nC, vc = d->batch * d->vheads * nC;
-    const size_t KP = (d->dkey + 31) / 32 * 32, VP = (d->dvalue + 31) / 32 * 32;
+    const size_t KP = key_steps(d) * 32, VP = (d->dvalue + 31) / 32 * 32;
     const auto take = [&o](size_t& at, size_t bytes) {
         at = o.total;
         o.total += (bytes + 255) / 256 * 256;
     };
-    const size_t rows = kc * in * (KP / 8) * kFrag * 2;
-    take(o.kf, rows);
-    take(o.ktf, rows);
-    take(o.qf, rows);
-    take(o.xf, vc * 3 * kTri * kFrag * 2);
-    take(o.vec, vc * 3 * kC * 4);
-    if (!bwd) {
-        take(o.pf, vc * (in == 3 ? 3 : 2) * kTri * kFrag * 2);
-        return o;
-    }
-    take(o.qtf, rows);
-    take(o.xtf, vc * 3 * kTri * kFrag * 2);
-    take(o.ptf, vc * 3 * kTri * kFrag * 2);
+    const size_t rows = kc * (f32 ? 3 : 1) * 64 * (KP <= 64 ? 64 : 128) * 2;
+    take(o.kr, rows);
+    take(o.qr, rows);
+    const size_t units = bwd ? block_units<float, true>() : f32 ? block_units<float, false>() : block_units<uint16_t, false>();
+    take(o.blk, vc * units * kFrag * 2);
+    if (!bwd) return o;
     take(o.states, vc * KP * VP * 4);
     take(o.after, vc * KP * VP * 4);
     take(o.news, vc * kC * VP * 4);
@@ -58,44 +60,67 @@ Layout layout(const ssm_delta_desc_t* d, bool bwd) {
     return o;
 }
 
-Params params(const ssm_delta_desc_t* d, const Layout& o, bool bwd, void* workspace) {
+Params params(const ssm_delta_desc_t* d, const Layout& o, bool bwd, void* workspace, const void* q, const void* k) {
     Params p{};
     char* w = static_cast<char*>(workspace);
-    const auto u16 = [w](size_t at) { return reinterpret_cast<uint16_t*>(w + at); };
-    const auto f32 = [w](size_t at) { return reinterpret_cast<float*>(w + at); };
-    p.kf = u16(o.kf); p.ktf = u16(o.ktf); p.qf = u16(o.qf); p.xf = u16(o.xf); p.vec = f32(o.vec);
+    p.q = q; p.k = k;
+    p.packed = !plain_rows(d, q, k);
+    // plain rows are only read through these
+    p.kr = p.packed ? reinterpret_cast<uint16_t*>(w + o.kr) : static_cast<uint16_t*>(const_cast<void*>(k));
+    p.qr = p.packed ? reinterpret_cast<uint16_t*>(w + o.qr) : static_cast<uint16_t*>(const_cast<void*>(q));
+    p.blk = reinterpret_cast<uint16_t*>(w + o.blk);
     if (bwd) {
-        p.qtf = u16(o.qtf); p.xtf = u16(o.xtf); p.ptf = u16(o.ptf);
-        p.states = f32(o.states); p.news = f32(o.news);
-    } else {
-        p.pf = u16(o.pf);
+        p.states = reinterpret_cast<float*>(w + o.states);
+        p.news = reinterpret_cast<float*>(w + o.news);
     }
     p.B = d->batch; p.L = d->seqlen; p.Hk = d->kheads; p.Hv = d->vheads; p.K = d->dkey; p.V = d->dvalue;
     p.nC = (d->seqlen + kC - 1) / kC;
     p.VP = (d->dvalue + 31) / 32 * 32;
-    p.nV = bwd ? p.VP / 16 : (d->dvalue + 15) / 16;
     p.scale = d->scale;
     return p;
 }
 
 dim3 grid(int64_t n) { return dim3(static_cast<unsigned>(n)); }
 
+template <typename T, int KS, bool OUT, int NW, int NBUF>
+void sweep(Params p, hipStream_t s) {
+    constexpr int units = OUT ? block_units<T, false>() : 1 + kSplit;
+    constexpr int lds = NBUF * Stage<T, KS, units, OUT>::kElements * 2;
+    static_assert(lds <= 160 * 1024, "LDS of a CU");
+    p.nV = ((OUT ? p.V : p.VP) + 16 * NW - 1) / (16 * NW);
+    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, OUT, NW, NBUF>), grid(p.B * p.Hv * p.nV), dim3(64 * NW), lds, s, p);
+}
+
+template <typename T, int KS, int NW, int NBUF>
+void adjoint(GradParams g, hipStream_t s) {
+    constexpr int lds = NBUF * Stage<T, KS, 2 * kSplit + 1, true>::kElements * 2;
+    static_assert(lds <= 160 * 1024, "LDS of a CU");
+    g.f.nV = (g.f.VP + 16 * NW - 1) / (16 * NW);
+    hipLaunchKernelGGL((delta_adjoint_kernel<T, KS, NW, NBUF>), grid(g.f.B * g.f.Hv * g.f.nV), dim3(64 * NW), lds, s,
+                       g);
+}
+
+template <typename T, int KS, bool BWD>
+void prepare(const Params& p, hipStream_t s) {
+    if (p.packed) hipLaunchKernelGGL((delta_pack_kernel<T, KS>), grid(p.B * p.Hk * p.nC), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_solve_kernel<T, KS, BWD>), grid(p.B * p.Hv * p.nC), dim3(256), 0, s, p);
+}
+
 template <typename T, int KS>
 int fwd(const Params& p, hipStream_t s) {
-    hipLaunchKernelGGL((delta_pack_kernel<T, KS, false>), grid(p.B * p.Hk * p.nC), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((delta_solve_kernel<T, KS, false>), grid(p.B * p.Hv * p.nC), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, true>), grid(p.B * p.Hv * p.nV), dim3(64), 0, s, p);
+    constexpr int nbuf = sizeof(T) == 4 ? 1 : 2;
+    prepare<T, KS, false>(p, s);
+    sweep<T, KS, true, 4, nbuf>(p, s);
     return ssm::launch_status();
 }
 
 template <typename T, int KS>
 int bwd(const GradParams& g, hipStream_t s) {
-    const Params& p = g.f;
-    hipLaunchKernelGGL((delta_pack_kernel<T, KS, true>), grid(p.B * p.Hk * p.nC), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((delta_solve_kernel<T, KS, true>), grid(p.B * p.Hv * p.nC), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, false>), grid(p.B * p.Hv * p.nV), dim3(64), 0, s, p);
-    hipLaunchKernelGGL((delta_adjoint_kernel<T, KS>), grid(p.B * p.Hv * p.nV), dim3(64), 0, s, g);
-    hipLaunchKernelGGL((delta_grad_kernel<T, KS>), grid(p.B * p.Hk * p.nC), dim3(256), 0, s, g);
+    constexpr int nbuf = sizeof(T) == 4 ? 1 : 2;
+    prepare<T, KS, true>(g.f, s);
+    sweep<T, KS, false, 4, nbuf>(g.f, s);
+    adjoint<T, KS, 4, nbuf>(g, s);
+    hipLaunchKernelGGL((delta_grad_kernel<T, KS>), grid(g.f.B * g.f.Hk * g.f.nC), dim3(256), 0, s, g);
     return ssm::launch_status();
 }
 
@@ -172,8 +197,9 @@ int ssm_delta_fwd(const ssm_delta_desc_t* d, const void* q, const void* k, const
     const Layout o = layout(d, false);
     if (!workspace || workspace_bytes < o.total) return SSM_ERR_WORKSPACE_TOO_SMALL;
     if (!ssm::aligned(workspace, 256)) return SSM_ERR_INVALID_ARGUMENT;
-    Params p = params(d, o, false, workspace);
-    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.h0 = h0; p.lengths = lengths; p.y = y; p.h_last = h_last;
+    Params p = params(d, o, false, workspace, q, k);
+    p.v = v; p.g = g; p.beta = beta; p.h0 = h0; p.lengths = lengths; p.y = y; p.h_last = h_last;
+    p.vec_v = d->dvalue * io_size(d) % 16 == 0 && ssm::aligned(v, 16);
     return by_size<Fwd>(d, p, static_cast<hipStream_t>(stream));
 }
 
@@ -208,12 +234,14 @@ int ssm_delta_bwd(const ssm_delta_desc_t* d, const void* q, const void* k, const
     if (!workspace || workspace_bytes < o.total) return SSM_ERR_WORKSPACE_TOO_SMALL;
     if (!ssm::aligned(workspace, 256)) return SSM_ERR_INVALID_ARGUMENT;
     GradParams p{};
-    p.f = params(d, o, true, workspace);
-    p.f.q = q; p.f.k = k; p.f.v = v; p.f.g = g; p.f.beta = beta; p.f.h0 = h0; p.f.lengths = lengths;
+    p.f = params(d, o, true, workspace, q, k);
+    p.f.v = v; p.f.g = g; p.f.beta = beta; p.f.h0 = h0; p.f.lengths = lengths;
     p.dy = dy; p.dh_last = dh_last; p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.dh0 = dh0;
     p.after = reinterpret_cast<float*>(static_cast<char*>(workspace) + o.after);
     p.dr = reinterpret_cast<float*>(static_cast<char*>(workspace) + o.dr);
-    p.vec_v = d->dvalue * io_size(d) % 16 == 0 && ssm::aligned(dy, 16);
+    const bool pieces = d->dvalue * io_size(d) % 16 == 0;
+    p.f.vec_v = pieces && ssm::aligned(v, 16);
+    p.vec_dy = pieces && ssm::aligned(dy, 16);
     return by_size<Bwd>(d, p, static_cast<hipStream_t>(stream));
 }
 

@@ -57,15 +57,28 @@ struct Params {
     const int32_t* lengths;
     void* y;
     float* h_last;
-    uint16_t *kf, *ktf, *qf, *qtf;  // [B][Hk][nC][planes][tiles][k steps] fragments (qtf: backward only)
-    uint16_t *xf, *xtf;             // [B][Hv][nC][3][6]
-    uint16_t *pf, *ptf;             // [B][Hv][nC][p_planes][6]
-    float* vec;                     // [B][Hv][nC][3][64]: e^G, e^{G_63 - G}, beta
+    // rows of k and q: the tensors themselves, or (packed) zero-padded bf16
+    // planes [B][Hk][nC][planes][64][pitch] that delta_pack_kernel wrote
+    uint16_t *kr, *qr;
+    uint16_t* blk;                  // [B][Hv][nC] blocks of fragments, see block_* below
     float *states, *news;           // backward: states entering each chunk (K x VP), E^ of each step (64 x VP)
     int64_t B, L, Hk, Hv, K, V, nC;
-    int64_t nV, VP;                 // 16-column tiles of the state, and their columns in all
+    int64_t nV, VP;                 // column groups of a workgroup, and the state's columns in all
     float scale;
+    int32_t packed, vec_v;          // kr, qr are packed; rows of v (and dy) move in 16-byte pieces
 };
+
+// A chunk's block: (backward: X^T, 18 fragments, P^T, 18) e^G, e^{G_63 - G} and
+// beta (64 floats each, one fragment's room), X (18), and, forward, P.
+constexpr int kSplit = 3 * kTri;  // fragments of a triangle in three planes
+template <bool BWD>
+struct Block {
+    static constexpr int kXt = 0, kPt = kSplit, kVec = BWD ? 2 * kSplit : 0, kX = kVec + 1, kP = kX + kSplit;
+};
+template <typename T, bool BWD>
+__host__ __device__ constexpr int block_units() {
+    return BWD ? 3 * kSplit + 1 : 1 + kSplit + (sizeof(T) == 4 ? kSplit : 2 * kTri);
+}
 
 __device__ __forceinline__ int tile_row(int t, int m) { return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3); }
 // fragment of triangle (tile t, k step s): lower triangles have s <= t / 2, upper ones s >= t / 2
@@ -143,45 +156,206 @@ struct PlanesOf<float> {
     static constexpr int kIn = 3, kOut = 3;
 };
 
-// Keys and queries of a chunk as fragments: rows = steps (kf, qf) and rows =
-// key elements (ktf, qtf).  Steps behind the row's length and elements behind
-// K are zeros.
-template <typename T, int KS, bool BWD>
+// ---- tiles of 64 rows in LDS.  A row is 16-byte pieces; piece p of row n sits
+// at p ^ f(n), chosen so that both kinds of reads spread over the banks: 16
+// rows of one piece (left operands whose rows are steps), and, transposed by
+// ds_read_b64_tr_b16, 4 rows x 4 pieces (left operands whose rows are key
+// elements).  Pitches are 128 elements (256 bytes: every bank once) or 64.
+template <int PITCH>
+__device__ __forceinline__ int swizzle(int n) {
+    return PITCH == 128 ? 4 * (n & 3) + ((n >> 3) & 3) : 4 * ((n >> 1) & 1) + ((n >> 3) & 3);
+}
+
+template <int KS>
+constexpr int pitch_of() {
+    return KS <= 2 ? 64 : 128;
+}
+
+__device__ __forceinline__ void wait_copies() {  // of this wave: vmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ void barrier() {  // every wave's LDS reads are done; copies stay in flight
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// `bytes` of memory from `base` (both the same in every lane) as a raw buffer
+__device__ __forceinline__ u32x4 window(const void* base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a))),
+                 static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a >> 32))) & 0xffffu,
+                 static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(bytes))), 0x00020000u};
+}
+
+// the same, for the compiler's own loads and stores
+__device__ __forceinline__ rsrc_t buffer(const void* base, uint32_t bytes) {
+    const u32x4 w = window(base, bytes);
+    return make_rsrc(reinterpret_cast<const void*>(w[0] | static_cast<uint64_t>(w[1]) << 32), w[2]);
+}
+
+// a generic pointer into LDS is the aperture's base with the offset in its low half
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+}
+
+// One copy of a wave: lane l's 16 bytes at `off` of the window go to
+// dst + 16 l of LDS, zeros where `off` is outside.  In assembly because the
+// compiler waits for every copy in flight before any read of LDS; here
+// wait_copies() and barrier() order the two, and the other buffer's copies
+// stay in flight.  No register receives anything.
+__device__ __forceinline__ void copy16(uint32_t dst, u32x4 from, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(from)
+                 : "memory");
+}
+
+constexpr uint32_t kNowhere = 0x40000000u;  // beyond every window, also with a row's offset added
+
+// Copies 64 rows of a tensor (`stride` elements apart, each of `pieces`
+// 16-byte pieces) into a tile; rows from `rows` on and pieces behind the last
+// become zeros.  The NW waves of the workgroup take turns.
+template <int PITCH, int NW>
+struct RowCopy {
+    static constexpr int kPer = 512 / PITCH, kPieces = PITCH / 8;  // rows of a copy, pieces of a row
+    static_assert(NW == 1 || NW * kPer % 8 == 0, "the waves' rows differ by whole eights or not at all");
+    // for copies whose first row is 8 f behind the wave's own first: all that
+    // the swizzle depends on beside the lane
+    uint32_t lane_off[4], step, first;
+
+    __device__ __forceinline__ RowCopy(int64_t stride, int pieces, int wave, int lane) {
+        step = static_cast<uint32_t>(stride) * 2;
+        first = wave * 1024;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int n = wave * kPer + lane / kPieces, piece = (lane % kPieces) ^ swizzle<PITCH>(n + 8 * f);
+            lane_off[f] = piece < pieces ? n * step + piece * 16 : kNowhere;
+        }
+    }
+    __device__ __forceinline__ void operator()(uint16_t* dst, const uint16_t* src, int rows) const {
+        const u32x4 w = window(src, static_cast<uint32_t>(rows) * step);
+        const uint32_t at = lds_offset(dst) + first;
+#pragma unroll
+        for (int i = 0; i < 64 / kPer; i += NW) copy16(at + i * 1024, w, lane_off[(i * kPer >> 3) & 3] + i * kPer * step);
+    }
+};
+
+// Copies UNITS KiB as they are.
+template <int UNITS, int NW>
+__device__ __forceinline__ void stage_block(uint16_t* dst, const uint16_t* src, int wave, int lane) {
+    const u32x4 w = window(src, UNITS * 1024);
+    const uint32_t at = lds_offset(dst) + wave * 1024, off = wave * 1024 + lane * 16;
+#pragma unroll
+    for (int i = 0; i < UNITS; i += NW)
+        if (i + NW <= UNITS || wave < UNITS - i) copy16(at + i * 1024, w, i * 1024 + off);
+}
+
+// Left operand whose rows are the 16 steps of tile t, k = elements 32 s ..
+template <int N, int PITCH>
+__device__ __forceinline__ Planes<N> row_frag(const uint16_t* tile, int t, int s, int lane) {
+    const int n = tile_row(t, lane & 15), piece = (4 * s + (lane >> 4)) ^ swizzle<PITCH>(n);
+    Planes<N> o;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        o.p[i] = *reinterpret_cast<const bf16x8*>(tile + i * 64 * PITCH + n * PITCH + piece * 8);
+    return o;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// 4 rows n .. n + 3 x 16 columns transposed: lane i of 16 gets column i's four
+// rows, having pointed at 4 elements of row i / 4 itself
+__device__ __forceinline__ s16x4 read_transposed(const uint16_t* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+}
+
+// Left operand whose rows are the 16 elements of tile t, k = steps 32 s ..
+template <int N, int PITCH>
+__device__ __forceinline__ Planes<N> col_frag(const uint16_t* tile, int t, int s, int lane) {
+    const int q = lane >> 4, r = (lane >> 2) & 3, c = lane & 3;
+    Planes<N> o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        s16x4 x[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = 32 * s + 8 * q + 4 * h + r, piece = (4 * (t >> 1) + c) ^ swizzle<PITCH>(n);
+            x[h] = read_transposed(tile + i * 64 * PITCH + n * PITCH + piece * 8 + 4 * (t & 1));
+        }
+        const s16x8 w = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        o.p[i] = __builtin_bit_cast(bf16x8, w);
+    }
+    return o;
+}
+
+// The 8 steps 32 s + 8 (l / 16) + 0 .. 7 of column `col16` + l % 16 of a tile of values (pitch 64)
+__device__ __forceinline__ void col_values(const uint16_t* tile, int s, int col16, int lane, float (&x)[8]) {
+    const int q = lane >> 4, r = (lane >> 2) & 3, c = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int n = 32 * s + 8 * q + 4 * h + r, piece = (col16 / 8 + (c >> 1)) ^ swizzle<64>(n);
+        const s16x4 v = read_transposed(tile + n * 64 + piece * 8 + 4 * (c & 1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[4 * h + j] = __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(v[j])) << 16);
+    }
+}
+
+// A chunk's keys or queries: rows of the tensor, or a packed tile
+template <typename T, int KS, int NW>
+struct KeyCopy {
+    static constexpr int kPitch = pitch_of<KS>(), kN = PlanesOf<T>::kIn;
+    RowCopy<kPitch, NW> copy;
+    int64_t head, step, plane;  // the head's first row, and elements from chunk to chunk and plane to plane
+    int64_t len;
+    bool packed;
+
+    __device__ __forceinline__ KeyCopy(const Params& p, int64_t b, int64_t hk, int64_t len, int wave, int lane)
+        : copy(kN > 1 || p.packed ? kPitch : p.Hk * p.K, kN > 1 || p.packed ? kPitch / 8 : static_cast<int>(p.K / 8),
+               wave, lane),
+          len(len), packed(kN > 1 || p.packed) {
+        plane = packed ? 64 * kPitch : 0;
+        step = packed ? kN * 64 * kPitch : kC * p.Hk * p.K;
+        head = packed ? (b * p.Hk + hk) * p.nC * step : (b * p.L * p.Hk + hk) * p.K;
+    }
+    __device__ __forceinline__ void operator()(uint16_t* dst, const uint16_t* x, int64_t c) const {
+        const int64_t left = len - c * kC;
+        const int rows = packed || left >= 64 ? 64 : static_cast<int>(left);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) copy(dst + i * 64 * kPitch, x + head + c * step + i * plane, rows);
+    }
+};
+
+// Keys and queries in zero-padded bf16 planes, where the tensors cannot be
+// copied as they are: fp32, or rows that are not 16-byte pieces.
+template <typename T, int KS>
 __global__ void __launch_bounds__(256) delta_pack_kernel(Params p) {
-    constexpr int kN = PlanesOf<T>::kIn, kRow = 32 * KS + 2;
-    __shared__ float s_x[kC][kRow];
-    const int tid = threadIdx.x;
+    constexpr int kN = PlanesOf<T>::kIn, kPitch = pitch_of<KS>();
     const int64_t c = blockIdx.x % p.nC, bh = blockIdx.x / p.nC, b = bh / p.Hk, h = bh % p.Hk;
-    const int64_t t0 = c * kC;
-    const int64_t len = row_len(p.lengths, b, p.L);
+    const int64_t t0 = c * kC, len = row_len(p.lengths, b, p.L);
     if (t0 >= len) return;
-    const int64_t unit = static_cast<int64_t>(kN) * 4 * KS * kFrag, at = static_cast<int64_t>(blockIdx.x) * unit;
     for (int which = 0; which < 2; ++which) {
         const T* src = static_cast<const T*>(which ? p.q : p.k);
-        for (int i = tid; i < kC * 32 * KS; i += 256) {
-            const int t = i / (32 * KS), e = i % (32 * KS);
-            const bool ok = t0 + t < len && e < p.K;
-            s_x[t][e] = ok ? Elem<T>::load(src, ((b * p.L + t0 + t) * p.Hk + h) * p.K + e) : 0.f;
-        }
-        __syncthreads();
-        uint16_t* rows = (which ? p.qf : p.kf) + at;
-        uint16_t* cols = which ? (BWD ? p.qtf + at : nullptr) : p.ktf + at;
-        for (int i = tid; i < 4 * KS * 64; i += 256) {
-            const int lane = i & 63, f = i >> 6, t = f / KS, s = f % KS;
+        uint16_t* dst = (which ? p.qr : p.kr) + static_cast<int64_t>(blockIdx.x) * kN * 64 * kPitch;
+        for (int i = threadIdx.x; i < 64 * kPitch / 8; i += 256) {
+            const int t = i / (kPitch / 8), e0 = i % (kPitch / 8) * 8;
+            const T* row = src + ((b * p.L + t0 + t) * p.Hk + h) * p.K;
             float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = s_x[tile_row(t, lane & 15)][32 * s + 8 * (lane >> 4) + j];
-            put_frag<kN>(rows, f, 4 * KS, lane, x);
-        }
-        if (cols)
-            for (int i = tid; i < 4 * KS * 64; i += 256) {
-                const int lane = i & 63, f = i >> 6, t = f / 2, s = f % 2;
-                float x[8];
+            for (int j = 0; j < 8; ++j) x[j] = t0 + t < len && e0 + j < p.K ? Elem<T>::load(row, e0 + j) : 0.f;
+            Planes<kN> o;
+            split8<kN>(x, o);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = s_x[32 * s + 8 * (lane >> 4) + j][tile_row(t, lane & 15)];
-                put_frag<kN>(cols, f, 4 * KS, lane, x);
-            }
-        __syncthreads();
+            for (int n = 0; n < kN; ++n) *reinterpret_cast<bf16x8*>(dst + n * 64 * kPitch + t * kPitch + e0) = o.p[n];
+        }
     }
 }
 
@@ -189,17 +363,21 @@ __global__ void __launch_bounds__(256) delta_pack_kernel(Params p) {
 // differences, not their size, set a decay's error).
 template <typename T, int KS, bool BWD>
 __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
-    constexpr int kN = PlanesOf<T>::kIn, kP = BWD ? 3 : PlanesOf<T>::kOut, kRow = kC + 4;
+    constexpr int kN = PlanesOf<T>::kIn, kP = PlanesOf<T>::kOut, kRow = kC + 4, kPitch = pitch_of<KS>();
+    __shared__ __align__(16) uint16_t s_k[kN * 64 * kPitch], s_q[kN * 64 * kPitch];
     __shared__ float s_a[kC][kRow], s_p[kC][kRow];
     __shared__ double s_g[kC];
     __shared__ float s_b[kC];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t c = blockIdx.x % p.nC, bh = blockIdx.x / p.nC, b = bh / p.Hv, h = bh % p.Hv;
+    using Blk = Block<BWD>;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t c = blockIdx.x % p.nC, bh = blockIdx.x / p.nC, b = bh / p.Hv, h = bh % p.Hv, hk = h / (p.Hv / p.Hk);
     const int64_t t0 = c * kC;
     const int64_t len = row_len(p.lengths, b, p.L);
     if (t0 >= len) return;
-    const int64_t kunit = static_cast<int64_t>(kN) * 4 * KS * kFrag;
-    const int64_t kat = ((b * p.Hk + h / (p.Hv / p.Hk)) * p.nC + c) * kunit;
+    uint16_t* blk = p.blk + static_cast<int64_t>(blockIdx.x) * block_units<T, BWD>() * kFrag;
+    const KeyCopy<T, KS, 4> keys(p, b, hk, len, wave, lane);
+    keys(s_k, p.kr, c);
+    keys(s_q, p.qr, c);
     if (wave == 0) {
         const bool ok = t0 + lane < len;
         const int64_t i = (b * p.L + t0 + lane) * p.Hv + h;
@@ -214,11 +392,12 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
         const double last = __shfl(G, 63, 64);
         s_g[lane] = G;
         s_b[lane] = be;
-        float* vec = p.vec + static_cast<int64_t>(blockIdx.x) * 3 * kC;
+        float* vec = reinterpret_cast<float*>(blk + Blk::kVec * kFrag);
         vec[lane] = expf(static_cast<float>(G));
         vec[kC + lane] = expf(static_cast<float>(last - G));
         vec[2 * kC + lane] = be;
     }
+    wait_copies();
     __syncthreads();
     // rows of tile `wave` against the steps not behind them
     f32x4 kk[4], qk[4];
@@ -227,12 +406,12 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
     const int ntile = wave < 2 ? 2 : 4;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-        const Planes<kN> ka = frag<kN>(p.kf + kat, wave * KS + s, 4 * KS, lane);
-        const Planes<kN> qa = frag<kN>(p.qf + kat, wave * KS + s, 4 * KS, lane);
+        const Planes<kN> ka = row_frag<kN, kPitch>(s_k, wave, s, lane);
+        const Planes<kN> qa = row_frag<kN, kPitch>(s_q, wave, s, lane);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
             if (t < ntile) {
-                const Planes<kN> kb = frag<kN>(p.kf + kat, t * KS + s, 4 * KS, lane);
+                const Planes<kN> kb = row_frag<kN, kPitch>(s_k, t, s, lane);
                 kk[t] = mma<3>(ka, kb, kk[t]);
                 qk[t] = mma<3>(qa, kb, qk[t]);
             }
@@ -265,28 +444,26 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
         }
     }
     __syncthreads();
-    uint16_t* xf = p.xf + static_cast<int64_t>(blockIdx.x) * 3 * kTri * kFrag;
-    uint16_t* pf = p.pf + static_cast<int64_t>(blockIdx.x) * kP * kTri * kFrag;
     for (int i = tid; i < 8 * 64; i += 256) {
         const int l = i & 63, t = i >> 7, s = (i >> 6) & 1;
         float x[8];
         if (s <= t / 2) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = s_a[tile_row(t, l & 15)][32 * s + 8 * (l >> 4) + j];
-            put_frag<3>(xf, tri_lower(t, s), kTri, l, x);
+            put_frag<3>(blk + Blk::kX * kFrag, tri_lower(t, s), kTri, l, x);
             if (!BWD) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = s_p[tile_row(t, l & 15)][32 * s + 8 * (l >> 4) + j];
-                put_frag<kP>(pf, tri_lower(t, s), kTri, l, x);
+                put_frag<kP>(blk + Blk::kP * kFrag, tri_lower(t, s), kTri, l, x);
             }
         }
         if (BWD && s >= t / 2) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = s_a[32 * s + 8 * (l >> 4) + j][tile_row(t, l & 15)];
-            put_frag<3>(p.xtf + static_cast<int64_t>(blockIdx.x) * 3 * kTri * kFrag, tri_upper(t, s), kTri, l, x);
+            put_frag<3>(blk + Blk::kXt * kFrag, tri_upper(t, s), kTri, l, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = s_p[32 * s + 8 * (l >> 4) + j][tile_row(t, l & 15)];
-            put_frag<3>(p.ptf + static_cast<int64_t>(blockIdx.x) * 3 * kTri * kFrag, tri_upper(t, s), kTri, l, x);
+            put_frag<3>(blk + Blk::kPt * kFrag, tri_upper(t, s), kTri, l, x);
         }
     }
 }
@@ -298,59 +475,142 @@ __device__ __forceinline__ void load8(const float* base, float (&x)[8]) {
     for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
 }
 
-// A wave's 16 columns of the state, as accumulator tiles
+// A wave's 16 columns of the state, as accumulator tiles: lane l has the
+// elements 32 s + 8 (l / 16) + 0 .. 7 of its column in tiles 2s, 2s + 1.
 template <int KS>
 __device__ __forceinline__ void load_state(const float* h, int64_t K, bool ok, int lane, f32x4 (&S)[2 * KS]) {
-    const int q = lane >> 4;
+    const int e0 = 8 * (lane >> 4);
+    if (!h) {
 #pragma unroll
-    for (int t = 0; t < 2 * KS; ++t)
+        for (int t = 0; t < 2 * KS; ++t) S[t] = zero4();
+    } else if (K % 4 == 0 && reinterpret_cast<uintptr_t>(h) % 16 == 0) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int e = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r;
-            S[t][r] = h && ok && e < K ? h[e] : 0.f;
+        for (int t = 0; t < 2 * KS; ++t) {
+            const int e = 32 * (t >> 1) + e0 + 4 * (t & 1);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(h + (e < K ? e : 0));
+            S[t] = ok && e < K ? x : zero4();
         }
+    } else {
+#pragma unroll
+        for (int t = 0; t < 2 * KS; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int e = 32 * (t >> 1) + e0 + 4 * (t & 1) + r;
+                const float x = h[e < K ? e : 0];
+                S[t][r] = ok && e < K ? x : 0.f;
+            }
+    }
 }
 
 template <int KS>
 __device__ __forceinline__ void store_state(float* h, int64_t K, bool ok, int lane, const f32x4 (&S)[2 * KS]) {
-    const int q = lane >> 4;
+    const int e0 = 8 * (lane >> 4);
+    const bool pieces = K % 4 == 0 && reinterpret_cast<uintptr_t>(h) % 16 == 0;
 #pragma unroll
-    for (int t = 0; t < 2 * KS; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int e = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r;
-            if (ok && e < K) h[e] = S[t][r];
+    for (int t = 0; t < 2 * KS; ++t) {
+        const int e = 32 * (t >> 1) + e0 + 4 * (t & 1);
+        if (pieces) {
+            if (ok && e < K) *reinterpret_cast<f32x4*>(h + e) = S[t];
+            continue;
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (ok && e + r < K) h[e + r] = S[t][r];
+    }
 }
 
-// The recurrence over chunks: one wave per 16 columns of a head's state.
+// Rows of fp32 in the workspace (`VP` to a row) from this lane's accumulators
+__device__ __forceinline__ void put_row(rsrc_t w, uint32_t lane_off, int row, uint32_t pitch, float x) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), w, lane_off + row * pitch, 0, 0);
+}
+
+// What a workgroup of the sweeps keeps in LDS for one chunk, in elements.  `blk`
+// units of 1 KiB, one tile of values (bf16 only), keys, queries (where read).
+template <typename T, int KS, int UNITS, bool QUERIES>
+struct Stage {
+    static constexpr int kTile = PlanesOf<T>::kIn * 64 * pitch_of<KS>();
+    static constexpr int kBlk = 0, kK = UNITS * kFrag, kQ = kK + kTile, kV = kQ + (QUERIES ? kTile : 0);
+    static constexpr int kElements = kV + (sizeof(T) == 2 ? 64 * 64 : 0);
+};
+
+// The recurrence over chunks: one wave per 16 columns of a head's state, NW
+// waves (neighbouring columns) sharing what is staged in LDS.  With two
+// buffers the next chunk's copies run under this chunk's products.
 // OUT: writes y and h_last (the forward); else the states entering each chunk
 // and E^ (what the gradients read).
-template <typename T, int KS, bool OUT>
-__global__ void __launch_bounds__(64) delta_chunk_kernel(Params p) {
-    constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut;
-    const int lane = threadIdx.x, q = lane >> 4;
+template <typename T, int KS, bool OUT, int NW, int NBUF>
+__global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
+    constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
+    constexpr int kUnits = OUT ? block_units<T, false>() : 1 + kSplit;
+    using St = Stage<T, KS, kUnits, OUT>;
+    using Blk = Block<!OUT>;
+    extern __shared__ __align__(16) uint16_t smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
     const int64_t VP = p.VP, vt = blockIdx.x % p.nV, bh = blockIdx.x / p.nV, b = bh / p.Hv, h = bh % p.Hv;
-    const int64_t col = vt * 16 + (lane & 15);
-    const bool ok = col < p.V;
-    const int64_t len = row_len(p.lengths, b, p.L);
+    const int64_t hk = h / (p.Hv / p.Hk);
+    const int64_t col0 = vt * 16 * NW, col = col0 + 16 * wave + (lane & 15);
+    const bool ok = col < p.V, tail = OUT || col < VP;
+    const int64_t len = row_len(p.lengths, b, p.L), chunks = (len + kC - 1) / kC;
+    const T* v = static_cast<const T*>(p.v) + (b * p.L * p.Hv + h) * p.V;
+    T* y = static_cast<T*>(p.y) + (b * p.L * p.Hv + h) * p.V;
+    const int64_t vstride = p.Hv * p.V;
+    const bool vtile = sizeof(T) == 2 && p.vec_v;
+
+    const KeyCopy<T, KS, NW> keys(p, b, hk, len, wave, lane);
+    const int64_t cols = p.V - col0;
+    const RowCopy<64, NW> values(vstride, static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
+    const auto issue = [&](int64_t c) {
+        uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
+        const uint16_t* blk = p.blk + (bh * p.nC + c) * block_units<T, !OUT>() * kFrag;
+        stage_block<kUnits, NW>(st, blk + Blk::kVec * kFrag, wave, lane);
+        keys(st + St::kK, p.kr, c);
+        if constexpr (OUT) keys(st + St::kQ, p.qr, c);
+        if (vtile) {
+            const int64_t left = len - c * kC;
+            values(st + St::kV, reinterpret_cast<const uint16_t*>(v) + c * kC * vstride + col0,
+                   left < 64 ? static_cast<int>(left) : 64);
+        }
+    };
+
     f32x4 S[2 * KS];
     load_state<KS>(p.h0 ? p.h0 + (bh * p.V + (ok ? col : 0)) * p.K : nullptr, p.K, ok, lane, S);
-    const T* v = static_cast<const T*>(p.v);
-    T* y = static_cast<T*>(p.y);
-    const int64_t kunit = static_cast<int64_t>(kN) * 4 * KS * kFrag;
-    const int64_t kat = (b * p.Hk + h / (p.Hv / p.Hk)) * p.nC * kunit;
-    for (int64_t c = 0; c * kC < len; ++c) {
+    float out[2][8];  // y of the chunk before, stored under this chunk's products
+    const uint32_t ystep = static_cast<uint32_t>(vstride * sizeof(T));
+    const uint32_t yoff = ok ? 8 * q * ystep + static_cast<uint32_t>(col * sizeof(T)) : kNowhere;
+    const auto put_out = [&](int64_t c) {  // rows behind the length are outside the window
+        const int64_t left = len - c * kC;
+        const rsrc_t w = buffer(y + c * kC * vstride, static_cast<uint32_t>(left < 64 ? left : 64) * ystep);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                Buf<T>::store(w, yoff + (32 * s + j) * ystep, out[s][j]);
+    };
+    const uint32_t pitch = static_cast<uint32_t>(VP * 4);
+    const uint32_t row_off = tail ? 8 * q * pitch + static_cast<uint32_t>(col * 4) : kNowhere;
+    if (NBUF == 2 && chunks > 0) issue(0);
+    for (int64_t c = 0; c < chunks; ++c) {
+        if constexpr (NBUF == 2) {
+            wait_copies();
+            barrier();
+            if (c + 1 < chunks) issue(c + 1);
+        } else {
+            barrier();
+            issue(c);
+            wait_copies();
+            barrier();
+        }
+        if (OUT && c > 0) put_out(c - 1);
+        const uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
+        const float* vec = reinterpret_cast<const float*>(st);
+        const uint16_t *xf = st + kFrag, *pf = st + (1 + kSplit) * kFrag;
         const int64_t t0 = c * kC, bhc = bh * p.nC + c;
-        const uint16_t *kf = p.kf + kat + c * kunit, *ktf = p.ktf + kat + c * kunit, *qf = p.qf + kat + c * kunit;
-        const uint16_t *xf = p.xf + bhc * 3 * kTri * kFrag, *pf = p.pf + bhc * kO * kTri * kFrag;
-        const float* vec = p.vec + bhc * 3 * kC;
         if constexpr (!OUT) {
-            float* st = p.states + bhc * (32 * KS) * VP + col;
+            const rsrc_t w = buffer(p.states + bhc * (32 * KS) * VP, 32 * KS * pitch);
 #pragma unroll
             for (int t = 0; t < 2 * KS; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) st[(32 * (t >> 1) + 8 * q + 4 * (t & 1) + r) * VP] = S[t][r];
+                for (int r = 0; r < 4; ++r) put_row(w, row_off, 32 * (t >> 1) + 4 * (t & 1) + r, pitch, S[t][r]);
         }
         Planes<3> Sp[KS];
 #pragma unroll
@@ -370,21 +630,29 @@ __global__ void __launch_bounds__(64) delta_chunk_kernel(Params p) {
             for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    ks[t] = mma<3>(frag<kN>(kf, (2 * s2 + t) * KS + s, 4 * KS, lane), Sp[s], ks[t]);
+                    ks[t] = mma<3>(row_frag<kN, kPitch>(st + St::kK, 2 * s2 + t, s, lane), Sp[s], ks[t]);
             float ga[8], x[8];
             load8(vec + 32 * s2 + 8 * q, ga);
             load8(vec + 2 * kC + 32 * s2 + 8 * q, be[s2]);
+            if (vtile) {
+                col_values(st + St::kV, s2, 16 * wave, lane, x);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int64_t t = t0 + 32 * s2 + 8 * q + j;
+                    x[j] = ok && t < len ? Elem<T>::load(v, t * vstride + col) : 0.f;
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int64_t t = t0 + 32 * s2 + 8 * q + j;
-                const float vv = ok && t < len ? Elem<T>::load(v, ((b * p.L + t) * p.Hv + h) * p.V + col) : 0.f;
-                E[s2][j] = vv - ga[j] * ks[j >> 2][j & 3];
+                E[s2][j] = x[j] - ga[j] * ks[j >> 2][j & 3];
                 x[j] = be[s2][j] * E[s2][j];
             }
             split8<3>(x, Y[s2]);
         }
         Planes<kO> U[2];
         Planes<3> W[2];
+        const rsrc_t wn = buffer(OUT ? nullptr : p.news + bhc * kC * VP, kC * pitch);
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
             float x[8], w[8];
@@ -398,13 +666,12 @@ __global__ void __launch_bounds__(64) delta_chunk_kernel(Params p) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float e = E[s2][4 * t + r] - a[r];
-                    if constexpr (!OUT)
-                        p.news[(bhc * kC + 32 * s2 + 8 * q + 4 * t + r) * VP + col] = e;
+                    if constexpr (!OUT) put_row(wn, row_off, 32 * s2 + 4 * t + r, pitch, e);
                     x[4 * t + r] = be[s2][4 * t + r] * e;
                     w[4 * t + r] *= x[4 * t + r];
                 }
             }
-            split8<kO>(x, U[s2]);
+            if constexpr (OUT) split8<kO>(x, U[s2]);
             split8<3>(w, W[s2]);
         }
         if constexpr (OUT) {
@@ -417,17 +684,14 @@ __global__ void __launch_bounds__(64) delta_chunk_kernel(Params p) {
                     f32x4 a = zero4();
 #pragma unroll
                     for (int s = 0; s < KS; ++s)
-                        a = mma<kO>(frag<kN>(qf, (2 * s2 + t) * KS + s, 4 * KS, lane), Sp[s], a);
+                        a = mma<kO>(row_frag<kN, kPitch>(st + St::kQ, 2 * s2 + t, s, lane), Sp[s], a);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) a[r] *= ga[4 * t + r] * p.scale;
 #pragma unroll
                     for (int s = 0; s <= s2; ++s)
                         a = mma<kO>(frag<kO>(pf, tri_lower(2 * s2 + t, s), kTri, lane), U[s], a);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int64_t i = t0 + 32 * s2 + 8 * q + 4 * t + r;
-                        if (ok && i < len) Elem<T>::store(y, ((b * p.L + i) * p.Hv + h) * p.V + col, a[r]);
-                    }
+                    for (int r = 0; r < 4; ++r) out[s2][4 * t + r] = a[r];
                 }
             }
         }
@@ -436,10 +700,11 @@ __global__ void __launch_bounds__(64) delta_chunk_kernel(Params p) {
         for (int t = 0; t < 2 * KS; ++t) {
             f32x4 a = S[t] * end;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) a = mma<3>(frag<kN>(ktf, 2 * t + s, 4 * KS, lane), W[s], a);
+            for (int s = 0; s < 2; ++s) a = mma<3>(col_frag<kN, kPitch>(st + St::kK, t, s, lane), W[s], a);
             S[t] = a;
         }
     }
+    if (OUT && chunks > 0) put_out(chunks - 1);
     if (OUT && p.h_last) store_state<KS>(p.h_last + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
 }
 

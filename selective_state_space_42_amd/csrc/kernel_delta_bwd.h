@@ -30,36 +30,73 @@ struct GradParams {
     void *dq, *dk, *dv, *dg, *dbeta;
     float* dh0;
     float *after, *dr;  // gradients of the states behind each chunk (K x VP), dR of each step (64 x VP)
-    int32_t vec_v;      // rows of dy move in 16-byte pieces
+    int32_t vec_dy;     // rows of dy move in 16-byte pieces
 };
 
-template <typename T, int KS>
-__global__ void __launch_bounds__(64) delta_adjoint_kernel(GradParams gp) {
-    constexpr int kN = PlanesOf<T>::kIn;
+// The mirror of delta_chunk_kernel, backwards over the chunks.
+template <typename T, int KS, int NW, int NBUF>
+__global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp) {
+    constexpr int kN = PlanesOf<T>::kIn, kPitch = pitch_of<KS>(), kUnits = 2 * kSplit + 1;
+    using St = Stage<T, KS, kUnits, true>;
+    using Blk = Block<true>;
+    extern __shared__ __align__(16) uint16_t smem[];
     const Params& p = gp.f;
-    const int lane = threadIdx.x, q = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
     const int64_t VP = p.VP, vt = blockIdx.x % p.nV, bh = blockIdx.x / p.nV, b = bh / p.Hv, h = bh % p.Hv;
-    const int64_t col = vt * 16 + (lane & 15);
-    const bool ok = col < p.V;
+    const int64_t hk = h / (p.Hv / p.Hk);
+    const int64_t col0 = vt * 16 * NW, col = col0 + 16 * wave + (lane & 15);
+    const bool ok = col < p.V, tail = col < VP;
     const int64_t len = row_len(p.lengths, b, p.L), chunks = (len + kC - 1) / kC;
+    const int64_t vstride = p.Hv * p.V;
+    const T* dy = static_cast<const T*>(gp.dy) + (b * p.L * p.Hv + h) * p.V;
+    T* dv = static_cast<T*>(gp.dv) + (b * p.L * p.Hv + h) * p.V;
+    const bool vtile = sizeof(T) == 2 && gp.vec_dy;
+
+    const KeyCopy<T, KS, NW> keys(p, b, hk, len, wave, lane);
+    const int64_t cols = p.V - col0;
+    const RowCopy<64, NW> values(vstride, static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
+    const auto issue = [&](int64_t c) {
+        uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
+        stage_block<kUnits, NW>(st, p.blk + (bh * p.nC + c) * block_units<T, true>() * kFrag, wave, lane);
+        keys(st + St::kK, p.kr, c);
+        keys(st + St::kQ, p.qr, c);
+        if (vtile) {
+            const int64_t left = len - c * kC;
+            values(st + St::kV, reinterpret_cast<const uint16_t*>(dy) + c * kC * vstride + col0,
+                   left < 64 ? static_cast<int>(left) : 64);
+        }
+    };
+    const uint32_t pitch = static_cast<uint32_t>(VP * 4), ystep = static_cast<uint32_t>(vstride * sizeof(T));
+    const uint32_t row_off = tail ? 8 * q * pitch + static_cast<uint32_t>(col * 4) : kNowhere;
+    const uint32_t yoff = ok ? 8 * q * ystep + static_cast<uint32_t>(col * sizeof(T)) : kNowhere;
+
     f32x4 S[2 * KS];
     load_state<KS>(gp.dh_last ? gp.dh_last + (bh * p.V + (ok ? col : 0)) * p.K : nullptr, p.K, ok, lane, S);
-    const T* dy = static_cast<const T*>(gp.dy);
-    T* dv = static_cast<T*>(gp.dv);
-    const int64_t kunit = static_cast<int64_t>(kN) * 4 * KS * kFrag;
-    const int64_t kat = (b * p.Hk + h / (p.Hv / p.Hk)) * p.nC * kunit;
     for (int64_t t = chunks * kC + q; t < p.L; t += 4)
-        if (ok) Elem<T>::store(dv, ((b * p.L + t) * p.Hv + h) * p.V + col, 0.f);
+        if (ok) Elem<T>::store(dv, t * vstride + col, 0.f);
+    if (NBUF == 2 && chunks > 0) issue(chunks - 1);
     for (int64_t c = chunks - 1; c >= 0; --c) {
+        if constexpr (NBUF == 2) {
+            wait_copies();
+            barrier();
+            if (c > 0) issue(c - 1);
+        } else {
+            barrier();
+            issue(c);
+            wait_copies();
+            barrier();
+        }
+        const uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
+        const float* vec = reinterpret_cast<const float*>(st + Blk::kVec * kFrag);
+        const uint16_t *xtf = st + Blk::kXt * kFrag, *ptf = st + Blk::kPt * kFrag;
         const int64_t t0 = c * kC, bhc = bh * p.nC + c;
-        const uint16_t *kf = p.kf + kat + c * kunit, *ktf = p.ktf + kat + c * kunit, *qtf = p.qtf + kat + c * kunit;
-        const uint16_t *xtf = p.xtf + bhc * 3 * kTri * kFrag, *ptf = p.ptf + bhc * 3 * kTri * kFrag;
-        const float* vec = p.vec + bhc * 3 * kC;
-        float* st = gp.after + bhc * (32 * KS) * VP + col;
+        const rsrc_t wa = buffer(gp.after + bhc * (32 * KS) * VP, 32 * KS * pitch);
+        const rsrc_t wr = buffer(gp.dr + bhc * kC * VP, kC * pitch);
+        const rsrc_t wv = buffer(dv + t0 * vstride, static_cast<uint32_t>(p.L - t0 < 64 ? p.L - t0 : 64) * ystep);
 #pragma unroll
         for (int t = 0; t < 2 * KS; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) st[(32 * (t >> 1) + 8 * q + 4 * (t & 1) + r) * VP] = S[t][r];
+            for (int r = 0; r < 4; ++r) put_row(wa, row_off, 32 * (t >> 1) + 4 * (t & 1) + r, pitch, S[t][r]);
         Planes<3> Sp[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -76,10 +113,14 @@ __global__ void __launch_bounds__(64) delta_adjoint_kernel(GradParams gp) {
             float x[8];
             load8(vec + 32 * s + 8 * q, ga[s]);
             load8(vec + 2 * kC + 32 * s + 8 * q, be[s]);
+            if (vtile) {
+                col_values(st + St::kV, s, 16 * wave, lane, x);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t t = t0 + 32 * s + 8 * q + j;
-                x[j] = ok && t < len ? Elem<T>::load(dy, ((b * p.L + t) * p.Hv + h) * p.V + col) : 0.f;
+                for (int j = 0; j < 8; ++j) {
+                    const int64_t t = t0 + 32 * s + 8 * q + j;
+                    x[j] = ok && t < len ? Elem<T>::load(dy, t * vstride + col) : 0.f;
+                }
             }
             split8<kN>(x, dO[s]);
 #pragma unroll
@@ -95,7 +136,7 @@ __global__ void __launch_bounds__(64) delta_adjoint_kernel(GradParams gp) {
                 f32x4 a = zero4();
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
-                    a = mma<3>(frag<kN>(kf, (2 * s2 + t) * KS + s, 4 * KS, lane), Sp[s], a);
+                    a = mma<3>(row_frag<kN, kPitch>(st + St::kK, 2 * s2 + t, s, lane), Sp[s], a);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) a[r] *= w[4 * t + r];
 #pragma unroll
@@ -122,9 +163,9 @@ __global__ void __launch_bounds__(64) delta_adjoint_kernel(GradParams gp) {
                 for (int r = 0; r < 4; ++r) {
                     const int j = 4 * t + r, i = 32 * s2 + 8 * q + j;
                     const float dr = du[s2][j] - a[r], de = be[s2][j] * dr;
-                    gp.dr[(bhc * kC + i) * VP + col] = dr;
-                    if (ok && t0 + i < p.L)
-                        Elem<T>::store(dv, ((b * p.L + t0 + i) * p.Hv + h) * p.V + col, t0 + i < len ? de : 0.f);
+                    put_row(wr, row_off, 32 * s2 + j, pitch, dr);
+                    Buf<T>::store(wv, yoff + (32 * s2 + j) * ystep,
+                                  t0 + i < len ? de : 0.f);
                     x[j] = -ga[s2][j] * de;
                 }
             }
@@ -136,8 +177,8 @@ __global__ void __launch_bounds__(64) delta_adjoint_kernel(GradParams gp) {
             f32x4 a = S[t] * end;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                a = mma<3>(frag<kN>(qtf, 2 * t + s, 4 * KS, lane), gO[s], a);
-                a = mma<3>(frag<kN>(ktf, 2 * t + s, 4 * KS, lane), gE[s], a);
+                a = mma<3>(col_frag<kN, kPitch>(st + St::kQ, t, s, lane), gO[s], a);
+                a = mma<3>(col_frag<kN, kPitch>(st + St::kK, t, s, lane), gE[s], a);
             }
             S[t] = a;
         }
@@ -187,11 +228,12 @@ __device__ __forceinline__ float sum_quarters(float x) {  // over the four lanes
 // to the next one's right operand in registers.
 template <typename T, int KS>
 __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
-    constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut;
+    constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
+    __shared__ __align__(16) uint16_t s_k[kN * 64 * kPitch], s_q[kN * 64 * kPitch];
     __shared__ double s_g[kC];
     __shared__ float s_dg[kC], s_db[kC], s_end[4];
     const Params& p = gp.f;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
     const int64_t c = blockIdx.x % p.nC, bh = blockIdx.x / p.nC, b = bh / p.Hk, hk = bh % p.Hk;
     const int64_t t0 = c * kC, group = p.Hv / p.Hk, VP = p.VP;
     const int64_t len = row_len(p.lengths, b, p.L);
@@ -202,7 +244,12 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
     f32x4 dq_all[2 * KS], dk_all[2 * KS];
 #pragma unroll
     for (int t = 0; t < 2 * KS; ++t) dq_all[t] = dk_all[t] = zero4();
-    const int64_t kunit = static_cast<int64_t>(kN) * 4 * KS * kFrag, kat = (bh * p.nC + c) * kunit;
+    if (t0 < len) {
+        const KeyCopy<T, KS, 4> keys(p, b, hk, len, wave, lane);
+        keys(s_k, p.kr, c);
+        keys(s_q, p.qr, c);
+        wait_copies();  // of this wave; the others' behind the first barrier
+    }
     for (int64_t hv = hk * group; hv < (hk + 1) * group; ++hv) {
         const int64_t gate = (b * p.L + t0 + lane) * p.Hv + hv;
         if (t0 >= len) {
@@ -213,7 +260,8 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
             continue;
         }
         const int64_t bhc = (b * p.Hv + hv) * p.nC + c;
-        const float* vec = p.vec + bhc * 3 * kC;
+        const float* vec =
+            reinterpret_cast<const float*>(p.blk + (bhc * block_units<T, true>() + Block<true>::kVec) * kFrag);
         float g_raw = 0.f;
         if (wave == 0) {
             g_raw = t0 + lane < len ? Elem<T>::load(static_cast<const T*>(p.g), gate) : 0.f;
@@ -240,7 +288,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
             float x[8], y[8];
             Planes<kN> On;
             Planes<kO> En, Un;
-            row8<T>(dyh + tn * p.Hv * p.V, v0, p.V, tn < len, gp.vec_v, x);
+            row8<T>(dyh + tn * p.Hv * p.V, v0, p.V, tn < len, gp.vec_dy, x);
             split8<kN>(x, On);
             load8(dr + n * VP + v0, x);
             load8(news + n * VP + v0, y);
@@ -283,7 +331,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
                 if (t / 2 >= wave / 2) {  // rows i not before them
                     Planes<kN> o;
                     Planes<kO> e;
-                    row8<T>(dyh + (t0 + m) * p.Hv * p.V, v0, p.V, t0 + m < len, gp.vec_v, x);
+                    row8<T>(dyh + (t0 + m) * p.Hv * p.V, v0, p.V, t0 + m < len, gp.vec_dy, x);
                     split8<kN>(x, o);
                     load8(dr + m * VP + v0, x);
 #pragma unroll
@@ -318,14 +366,14 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
 #pragma unroll
         for (int t = 0; t < 2 * KS; ++t) {
             f32x4 gq = D1[t] * ga_n, row = D2[t] * ga_n, col = D3[t] * w_n;
-            const Planes<kN> kr = frag<kN>(p.kf + kat, wave * KS + (t >> 1), 4 * KS, lane);
-            const Planes<kN> qr = frag<kN>(p.qf + kat, wave * KS + (t >> 1), 4 * KS, lane);
+            const Planes<kN> kr = row_frag<kN, kPitch>(s_k, wave, t >> 1, lane);
+            const Planes<kN> qr = row_frag<kN, kPitch>(s_q, wave, t >> 1, lane);
 #pragma unroll
             for (int r = 0; r < 4; ++r) kover += plane_sum(kr, 4 * (t & 1) + r) * col[r];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const Planes<kN> kt = frag<kN>(p.ktf + kat, 2 * t + s, 4 * KS, lane);
-                const Planes<kN> qt = frag<kN>(p.qtf + kat, 2 * t + s, 4 * KS, lane);
+                const Planes<kN> kt = col_frag<kN, kPitch>(s_k, t, s, lane);
+                const Planes<kN> qt = col_frag<kN, kPitch>(s_q, t, s, lane);
                 gq = mma<kO>(kt, a1[s], gq);
                 row = mma<kO>(kt, a2[s], row);
                 col = mma<kO>(qt, b1[s], col);
