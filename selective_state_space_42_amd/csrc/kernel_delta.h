@@ -359,15 +359,43 @@ __global__ void __launch_bounds__(256) delta_pack_kernel(Params p) {
     }
 }
 
+// 8 consecutive floats of `base` (16-byte aligned)
+__device__ __forceinline__ void load8(const float* base, float (&x)[8]) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(base), b = *reinterpret_cast<const f32x4*>(base + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+}
+
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+
+// c + a b for 16 x 16 fp32 blocks: row l % 16 of `a` (this lane's elements
+// 4 (l / 16) + 0 .. 3 of it) and `b` as an accumulator (rows 4 (l / 16) + r):
+// the k of instruction r is 4 (l / 16) + r on both sides.
+__device__ __forceinline__ f32x4 block_product(f32x4 a, f32x4 b, f32x4 c) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+    return c;
+}
+
 // Decays, X and P of a chunk.  The running sums of g are fp64 (their
 // differences, not their size, set a decay's error).
+//
+// X = (I + A' D)^-1 A' by forward substitution over blocks of 16 steps, as an
+// inverse by powers of A' D would lose all digits for like keys: with T_I the
+// inverse of the diagonal block I (16 rows, a lane a column, each wave one
+// block), X_I = T_I (A'_I - sum_{J < I} A'_IJ D_J X_J) in fp32 matrix
+// instructions, wave w keeping column block w of X in registers.
 template <typename T, int KS, bool BWD>
 __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
     constexpr int kN = PlanesOf<T>::kIn, kP = PlanesOf<T>::kOut, kRow = kC + 4, kPitch = pitch_of<KS>();
-    __shared__ __align__(16) uint16_t s_k[kN * 64 * kPitch], s_q[kN * 64 * kPitch];
-    __shared__ float s_a[kC][kRow], s_p[kC][kRow];
+    // the keys' and queries' tiles, then (once read) A' (later X) and P
+    constexpr int kTiles = 2 * kN * 64 * kPitch * 2, kMats = 2 * kC * kRow * 4;
+    __shared__ __align__(16) unsigned char s_buf[kTiles > kMats ? kTiles : kMats];
+    __shared__ __align__(16) float s_t[4][16][20], s_b[kC];
     __shared__ double s_g[kC];
-    __shared__ float s_b[kC];
+    uint16_t *s_k = reinterpret_cast<uint16_t*>(s_buf), *s_q = s_k + kN * 64 * kPitch;
+    float (*s_a)[kRow] = reinterpret_cast<float (*)[kRow]>(s_buf);
+    float (*s_p)[kRow] = s_a + kC;
     using Blk = Block<BWD>;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t c = blockIdx.x % p.nC, bh = blockIdx.x / p.nC, b = bh / p.Hv, h = bh % p.Hv, hk = h / (p.Hv / p.Hk);
@@ -416,6 +444,7 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
                 qk[t] = mma<3>(qa, kb, qk[t]);
             }
     }
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const int j = tile_row(t, lane & 15);
@@ -428,32 +457,50 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
         }
     }
     __syncthreads();
-    if (wave == 0) {
-        // X_i = A'_i - sum_{l < i} A'_il beta_l X_l, lane j holding column j; row i of A' is
-        // read whole before the lanes put X_i in its place
-        float x[kC];
+    {
+        // column lane % 16 of T: T_i = delta_i - sum_{l < i} A'_il beta_l T_l
+        const int o = 16 * wave, j = lane & 15;
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < kC; ++i) {
-            float acc = s_a[i][lane];
+        for (int i = 0; i < 16; ++i) {
+            float acc = i == j ? 1.f : 0.f;
 #pragma unroll
-            for (int l = 0; l < i; ++l) acc -= s_a[i][l] * s_b[l] * x[l];
-            x[i] = acc;
-            __builtin_amdgcn_wave_barrier();
-            s_a[i][lane] = acc;
-            __builtin_amdgcn_wave_barrier();
+            for (int l = 0; l < i; ++l) acc -= s_a[o + i][o + l] * x[l];
+            if (lane < 16) s_t[wave][i][j] = acc;
+            x[i] = acc * s_b[o + i];
         }
     }
+    __syncthreads();
+    const int q = lane >> 4, m = lane & 15;
+    f32x4 X[4];
+#pragma unroll
+    for (int I = 0; I < 4; ++I) {
+        X[I] = zero4();
+        if (I < wave) continue;
+        f32x4 a;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = s_a[16 * I + 4 * q + r][16 * wave + m];
+#pragma unroll
+        for (int J = 0; J < I; ++J)
+            if (J >= wave) a = block_product(load4(&s_a[16 * I + m][16 * J + 4 * q]) * -load4(&s_b[16 * J + 4 * q]), X[J], a);
+        X[I] = block_product(load4(&s_t[I][m][4 * q]), a, zero4());
+    }
+    __syncthreads();
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+        if (I >= wave)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s_a[16 * I + 4 * q + r][16 * wave + m] = X[I][r];
     __syncthreads();
     for (int i = tid; i < 8 * 64; i += 256) {
         const int l = i & 63, t = i >> 7, s = (i >> 6) & 1;
         float x[8];
         if (s <= t / 2) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = s_a[tile_row(t, l & 15)][32 * s + 8 * (l >> 4) + j];
+            const int row = tile_row(t, l & 15), col = 32 * s + 8 * (l >> 4);
+            load8(&s_a[row][col], x);
             put_frag<3>(blk + Blk::kX * kFrag, tri_lower(t, s), kTri, l, x);
             if (!BWD) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = s_p[tile_row(t, l & 15)][32 * s + 8 * (l >> 4) + j];
+                load8(&s_p[row][col], x);
                 put_frag<kP>(blk + Blk::kP * kFrag, tri_lower(t, s), kTri, l, x);
             }
         }
@@ -466,13 +513,6 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
             put_frag<3>(blk + Blk::kPt * kFrag, tri_upper(t, s), kTri, l, x);
         }
     }
-}
-
-// 8 consecutive floats of `base` (16-byte aligned)
-__device__ __forceinline__ void load8(const float* base, float (&x)[8]) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(base), b = *reinterpret_cast<const f32x4*>(base + 4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
 }
 
 // A wave's 16 columns of the state, as accumulator tiles: lane l has the
