@@ -27,7 +27,7 @@ int check_desc(const ssm_delta_desc_t* d) {
 }
 
 struct Layout {
-    size_t kr, qr, blk, states, news, after, dr, total;
+    size_t kr, qr, blk, slab, total;
 };
 
 int64_t key_steps(const ssm_delta_desc_t* d) { return (d->dkey + 31) / 32; }
@@ -53,10 +53,8 @@ Layout layout(const ssm_delta_desc_t* d, bool bwd) {
     const size_t units = bwd ? block_units<float, true>() : f32 ? block_units<float, false>() : block_units<uint16_t, false>();
     take(o.blk, vc * units * kFrag * 2);
     if (!bwd) return o;
-    take(o.states, vc * KP * VP * 4);
-    take(o.after, vc * KP * VP * 4);
-    take(o.news, vc * kC * VP * 4);
-    take(o.dr, vc * kC * VP * 4);
+    const size_t pitch = KP <= 64 ? 64 : 128, planes = f32 ? 3 : 2;
+    take(o.slab, vc * (VP / 32) * (planes * 32 * (2 * pitch + 2 * 64) + (f32 ? 3 : 1) * 32 * 64) * 2);
     return o;
 }
 
@@ -69,10 +67,7 @@ Params params(const ssm_delta_desc_t* d, const Layout& o, bool bwd, void* worksp
     p.kr = p.packed ? reinterpret_cast<uint16_t*>(w + o.kr) : static_cast<uint16_t*>(const_cast<void*>(k));
     p.qr = p.packed ? reinterpret_cast<uint16_t*>(w + o.qr) : static_cast<uint16_t*>(const_cast<void*>(q));
     p.blk = reinterpret_cast<uint16_t*>(w + o.blk);
-    if (bwd) {
-        p.states = reinterpret_cast<float*>(w + o.states);
-        p.news = reinterpret_cast<float*>(w + o.news);
-    }
+    if (bwd) p.slab = reinterpret_cast<uint16_t*>(w + o.slab);
     p.B = d->batch; p.L = d->seqlen; p.Hk = d->kheads; p.Hv = d->vheads; p.K = d->dkey; p.V = d->dvalue;
     p.nC = (d->seqlen + kC - 1) / kC;
     p.VP = (d->dvalue + 31) / 32 * 32;
@@ -120,7 +115,11 @@ int bwd(const GradParams& g, hipStream_t s) {
     prepare<T, KS, true>(g.f, s);
     sweep<T, KS, false, 4, nbuf>(g.f, s);
     adjoint<T, KS, 4, nbuf>(g, s);
-    hipLaunchKernelGGL((delta_grad_kernel<T, KS>), grid(g.f.B * g.f.Hk * g.f.nC), dim3(256), 0, s, g);
+    const dim3 chunks = grid(g.f.B * g.f.Hk * g.f.nC);
+    if (g.f.Hv > g.f.Hk)
+        hipLaunchKernelGGL((delta_grad_kernel<T, KS, true>), chunks, dim3(256), 0, s, g);
+    else
+        hipLaunchKernelGGL((delta_grad_kernel<T, KS, false>), chunks, dim3(256), 0, s, g);
     return ssm::launch_status();
 }
 
@@ -237,8 +236,6 @@ int ssm_delta_bwd(const ssm_delta_desc_t* d, const void* q, const void* k, const
     p.f = params(d, o, true, workspace, q, k);
     p.f.v = v; p.f.g = g; p.f.beta = beta; p.f.h0 = h0; p.f.lengths = lengths;
     p.dy = dy; p.dh_last = dh_last; p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.dh0 = dh0;
-    p.after = reinterpret_cast<float*>(static_cast<char*>(workspace) + o.after);
-    p.dr = reinterpret_cast<float*>(static_cast<char*>(workspace) + o.dr);
     const bool pieces = d->dvalue * io_size(d) % 16 == 0;
     p.f.vec_v = pieces && ssm::aligned(v, 16);
     p.vec_dy = pieces && ssm::aligned(dy, 16);

@@ -61,7 +61,7 @@ struct Params {
     // planes [B][Hk][nC][planes][64][pitch] that delta_pack_kernel wrote
     uint16_t *kr, *qr;
     uint16_t* blk;                  // [B][Hv][nC] blocks of fragments, see block_* below
-    float *states, *news;           // backward: states entering each chunk (K x VP), E^ of each step (64 x VP)
+    uint16_t* slab;                 // backward: what delta_grad_kernel reads of the sweeps, see Slab
     int64_t B, L, Hk, Hv, K, V, nC;
     int64_t nV, VP;                 // column groups of a workgroup, and the state's columns in all
     float scale;
@@ -278,7 +278,7 @@ __device__ __forceinline__ s16x4 read_transposed(const uint16_t* p) {
 }
 
 // Left operand whose rows are the 16 elements of tile t, k = steps 32 s ..
-template <int N, int PITCH>
+template <int N, int PITCH, int ROWS = 64>
 __device__ __forceinline__ Planes<N> col_frag(const uint16_t* tile, int t, int s, int lane) {
     const int q = lane >> 4, r = (lane >> 2) & 3, c = lane & 3;
     Planes<N> o;
@@ -288,7 +288,7 @@ __device__ __forceinline__ Planes<N> col_frag(const uint16_t* tile, int t, int s
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int n = 32 * s + 8 * q + 4 * h + r, piece = (4 * (t >> 1) + c) ^ swizzle<PITCH>(n);
-            x[h] = read_transposed(tile + i * 64 * PITCH + n * PITCH + piece * 8 + 4 * (t & 1));
+            x[h] = read_transposed(tile + (i * ROWS + n) * PITCH + piece * 8 + 4 * (t & 1));
         }
         const s16x8 w = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
         o.p[i] = __builtin_bit_cast(bf16x8, w);
@@ -559,9 +559,30 @@ __device__ __forceinline__ void store_state(float* h, int64_t K, bool ok, int la
     }
 }
 
-// Rows of fp32 in the workspace (`VP` to a row) from this lane's accumulators
-__device__ __forceinline__ void put_row(rsrc_t w, uint32_t lane_off, int row, uint32_t pitch, float x) {
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), w, lane_off + row * pitch, 0, 0);
+// What the sweeps of the backward pass leave for delta_grad_kernel: for each
+// (chunk, value head) and 32 columns v, in bf16 planes, tiles with a row for
+// each v (swizzled as in LDS): the state entering the chunk, the gradient of the one
+// behind it (pitch_of key elements a row), E^, dR and dY (64 steps a row).  A sweep's
+// lane holds 8 neighbours of one v, which is one 16-byte store.
+template <typename T, int KS>
+struct Slab {
+    static constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
+    static constexpr int kStateTile = kO * 32 * kPitch, kStepTile = kO * 32 * 64;
+    static constexpr int kS = 0, kDs = kStateTile, kE = 2 * kStateTile, kDr = kE + kStepTile, kDy = kDr + kStepTile;
+    static constexpr int kElements = kDy + kN * 32 * 64;
+};
+
+typedef uint32_t store4 __attribute__((ext_vector_type(4)));
+
+// planes of 8 neighbours (piece `piece`) of row v of a slab's tile at element `at`
+template <int N, int PITCH, int M>
+__device__ __forceinline__ void put_planes(rsrc_t w, uint32_t slab_off, int v, int at, int piece, const Planes<M>& x) {
+    static_assert(N <= M, "planes at hand");
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            __builtin_bit_cast(store4, x.p[n]), w,
+            slab_off + 2 * (at + (n * 32 + v) * PITCH + 8 * (piece ^ swizzle<PITCH>(v))), 0, 0);
 }
 
 // What a workgroup of the sweeps keeps in LDS for one chunk, in elements.  `blk`
@@ -589,7 +610,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
     const int64_t VP = p.VP, vt = blockIdx.x % p.nV, bh = blockIdx.x / p.nV, b = bh / p.Hv, h = bh % p.Hv;
     const int64_t hk = h / (p.Hv / p.Hk);
     const int64_t col0 = vt * 16 * NW, col = col0 + 16 * wave + (lane & 15);
-    const bool ok = col < p.V, tail = OUT || col < VP;
+    const bool ok = col < p.V;
     const int64_t len = row_len(p.lengths, b, p.L), chunks = (len + kC - 1) / kC;
     const T* v = static_cast<const T*>(p.v) + (b * p.L * p.Hv + h) * p.V;
     T* y = static_cast<T*>(p.y) + (b * p.L * p.Hv + h) * p.V;
@@ -626,8 +647,10 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
             for (int j = 0; j < 8; ++j)
                 Buf<T>::store(w, yoff + (32 * s + j) * ystep, out[s][j]);
     };
-    const uint32_t pitch = static_cast<uint32_t>(VP * 4);
-    const uint32_t row_off = tail ? 8 * q * pitch + static_cast<uint32_t>(col * 4) : kNowhere;
+    using Sl = Slab<T, KS>;
+    const uint32_t slab_off = col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
+    const uint32_t slab_bytes = static_cast<uint32_t>(VP / 32) * (Sl::kElements * 2);
+    const int slab_row = static_cast<int>(col % 32);
     if (NBUF == 2 && chunks > 0) issue(0);
     for (int64_t c = 0; c < chunks; ++c) {
         if constexpr (NBUF == 2) {
@@ -645,13 +668,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
         const float* vec = reinterpret_cast<const float*>(st);
         const uint16_t *xf = st + kFrag, *pf = st + (1 + kSplit) * kFrag;
         const int64_t t0 = c * kC, bhc = bh * p.nC + c;
-        if constexpr (!OUT) {
-            const rsrc_t w = buffer(p.states + bhc * (32 * KS) * VP, 32 * KS * pitch);
-#pragma unroll
-            for (int t = 0; t < 2 * KS; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) put_row(w, row_off, 32 * (t >> 1) + 4 * (t & 1) + r, pitch, S[t][r]);
-        }
+        const rsrc_t ws = buffer(OUT ? nullptr : p.slab + bhc * (slab_bytes / 2), slab_bytes);
         Planes<3> Sp[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -659,6 +676,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = S[2 * s + (j >> 2)][j & 3];
             split8<3>(x, Sp[s]);
+            if constexpr (!OUT) put_planes<kO, kPitch>(ws, slab_off, slab_row, Sl::kS, 4 * s + q, Sp[s]);
         }
         // E^ and U, two row tiles (32 steps) at a time: lane's steps 32 s + 8 q + 0 .. 7
         float E[2][8], be[2][8];
@@ -692,7 +710,6 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
         }
         Planes<kO> U[2];
         Planes<3> W[2];
-        const rsrc_t wn = buffer(OUT ? nullptr : p.news + bhc * kC * VP, kC * pitch);
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
             float x[8], w[8];
@@ -705,13 +722,13 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
                     a = mma<3>(frag<3>(xf, tri_lower(2 * s2 + t, s), kTri, lane), Y[s], a);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float e = E[s2][4 * t + r] - a[r];
-                    if constexpr (!OUT) put_row(wn, row_off, 32 * s2 + 4 * t + r, pitch, e);
-                    x[4 * t + r] = be[s2][4 * t + r] * e;
-                    w[4 * t + r] *= x[4 * t + r];
+                    const float e = E[s2][4 * t + r] - a[r], u = be[s2][4 * t + r] * e;
+                    x[4 * t + r] = OUT ? u : e;
+                    w[4 * t + r] *= u;
                 }
             }
-            if constexpr (OUT) split8<kO>(x, U[s2]);
+            split8<kO>(x, U[s2]);  // E^ without beta where it is kept for the gradients
+            if constexpr (!OUT) put_planes<kO, 64>(ws, slab_off, slab_row, Sl::kE, 4 * s2 + q, U[s2]);
             split8<3>(w, W[s2]);
         }
         if constexpr (OUT) {

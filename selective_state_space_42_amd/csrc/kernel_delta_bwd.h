@@ -29,7 +29,6 @@ struct GradParams {
     const float* dh_last;
     void *dq, *dk, *dv, *dg, *dbeta;
     float* dh0;
-    float *after, *dr;  // gradients of the states behind each chunk (K x VP), dR of each step (64 x VP)
     int32_t vec_dy;     // rows of dy move in 16-byte pieces
 };
 
@@ -45,7 +44,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
     const int64_t VP = p.VP, vt = blockIdx.x % p.nV, bh = blockIdx.x / p.nV, b = bh / p.Hv, h = bh % p.Hv;
     const int64_t hk = h / (p.Hv / p.Hk);
     const int64_t col0 = vt * 16 * NW, col = col0 + 16 * wave + (lane & 15);
-    const bool ok = col < p.V, tail = col < VP;
+    const bool ok = col < p.V;
     const int64_t len = row_len(p.lengths, b, p.L), chunks = (len + kC - 1) / kC;
     const int64_t vstride = p.Hv * p.V;
     const T* dy = static_cast<const T*>(gp.dy) + (b * p.L * p.Hv + h) * p.V;
@@ -66,8 +65,11 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
                    left < 64 ? static_cast<int>(left) : 64);
         }
     };
-    const uint32_t pitch = static_cast<uint32_t>(VP * 4), ystep = static_cast<uint32_t>(vstride * sizeof(T));
-    const uint32_t row_off = tail ? 8 * q * pitch + static_cast<uint32_t>(col * 4) : kNowhere;
+    using Sl = Slab<T, KS>;
+    const uint32_t slab_off = col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
+    const uint32_t slab_bytes = static_cast<uint32_t>(VP / 32) * (Sl::kElements * 2);
+    const int slab_row = static_cast<int>(col % 32);
+    const uint32_t ystep = static_cast<uint32_t>(vstride * sizeof(T));
     const uint32_t yoff = ok ? 8 * q * ystep + static_cast<uint32_t>(col * sizeof(T)) : kNowhere;
 
     f32x4 S[2 * KS];
@@ -90,13 +92,8 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
         const float* vec = reinterpret_cast<const float*>(st + Blk::kVec * kFrag);
         const uint16_t *xtf = st + Blk::kXt * kFrag, *ptf = st + Blk::kPt * kFrag;
         const int64_t t0 = c * kC, bhc = bh * p.nC + c;
-        const rsrc_t wa = buffer(gp.after + bhc * (32 * KS) * VP, 32 * KS * pitch);
-        const rsrc_t wr = buffer(gp.dr + bhc * kC * VP, kC * pitch);
+        const rsrc_t ws = buffer(p.slab + bhc * (slab_bytes / 2), slab_bytes);
         const rsrc_t wv = buffer(dv + t0 * vstride, static_cast<uint32_t>(p.L - t0 < 64 ? p.L - t0 : 64) * ystep);
-#pragma unroll
-        for (int t = 0; t < 2 * KS; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) put_row(wa, row_off, 32 * (t >> 1) + 4 * (t & 1) + r, pitch, S[t][r]);
         Planes<3> Sp[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -104,6 +101,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = S[2 * s + (j >> 2)][j & 3];
             split8<3>(x, Sp[s]);
+            put_planes<Sl::kO, kPitch>(ws, slab_off, slab_row, Sl::kDs, 4 * s + q, Sp[s]);
         }
         Planes<kN> dO[2];
         Planes<3> gO[2], Y[2], gE[2];
@@ -123,6 +121,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
                 }
             }
             split8<kN>(x, dO[s]);
+            put_planes<kN, 64>(ws, slab_off, slab_row, Sl::kDy, 4 * s + q, dO[s]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] *= ga[s][j] * p.scale;
             split8<3>(x, gO[s]);
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
         }
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
-            float x[8];
+            float x[8], dr[8];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 f32x4 a = zero4();
@@ -162,14 +161,17 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int j = 4 * t + r, i = 32 * s2 + 8 * q + j;
-                    const float dr = du[s2][j] - a[r], de = be[s2][j] * dr;
-                    put_row(wr, row_off, 32 * s2 + j, pitch, dr);
+                    dr[j] = du[s2][j] - a[r];
+                    const float de = be[s2][j] * dr[j];
                     Buf<T>::store(wv, yoff + (32 * s2 + j) * ystep,
                                   t0 + i < len ? de : 0.f);
                     x[j] = -ga[s2][j] * de;
                 }
             }
             split8<3>(x, gE[s2]);
+            Planes<Sl::kO> R;
+            split8<Sl::kO>(dr, R);
+            put_planes<Sl::kO, 64>(ws, slab_off, slab_row, Sl::kDr, 4 * s2 + q, R);
         }
         const float end = vec[kC - 1];
 #pragma unroll
@@ -184,28 +186,6 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
         }
     }
     if (gp.dh0) store_state<KS>(gp.dh0 + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
-}
-
-// 8 elements v0 .. v0 + 7 of a row of V elements, zeros behind its end or where !ok
-template <typename T>
-__device__ __forceinline__ void row8(const T* row, int64_t v0, int64_t V, bool ok, bool vec, float (&x)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 0.f;
-    if (!ok || v0 >= V) return;
-    if (vec) {
-        if constexpr (sizeof(T) == 2) {
-            const uint4 w = *reinterpret_cast<const uint4*>(row + v0);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(u[j]), x[2 * j + 1] = bf16_hi(u[j]);
-        } else {
-            load8(reinterpret_cast<const float*>(row + v0), x);
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (v0 + j < V) x[j] = Elem<T>::load(row, v0 + j);
 }
 
 template <int N>
@@ -225,17 +205,21 @@ __device__ __forceinline__ float sum_quarters(float x) {  // over the four lanes
 // A chunk's gradients, one workgroup per key head; wave w owns the 16 steps of
 // tile w as columns of every product (dQ^T, dK^T are K x 16), so the masked
 // 64 x 16 blocks of W1, W2 and their transposes pass from one product's result
-// to the next one's right operand in registers.
-template <typename T, int KS>
-__global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
+// to the next one's right operand in registers.  The products over v take 32
+// columns at a time from a slab; then the keys and queries take its place in LDS.
+template <typename T, int KS, bool GROUPED>
+__global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_grad_kernel(GradParams gp) {
     constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
-    __shared__ __align__(16) uint16_t s_k[kN * 64 * kPitch], s_q[kN * 64 * kPitch];
+    using Sl = Slab<T, KS>;
+    constexpr int kKeys = 2 * kN * 64 * kPitch;
+    __shared__ __align__(16) uint16_t s_buf[kKeys > Sl::kElements ? kKeys : Sl::kElements];
     __shared__ double s_g[kC];
     __shared__ float s_dg[kC], s_db[kC], s_end[4];
+    uint16_t *s_k = s_buf, *s_q = s_buf + kN * 64 * kPitch;
     const Params& p = gp.f;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
     const int64_t c = blockIdx.x % p.nC, bh = blockIdx.x / p.nC, b = bh / p.Hk, hk = bh % p.Hk;
-    const int64_t t0 = c * kC, group = p.Hv / p.Hk, VP = p.VP;
+    const int64_t t0 = c * kC, group = GROUPED ? p.Hv / p.Hk : 1;
     const int64_t len = row_len(p.lengths, b, p.L);
     const int n = tile_row(wave, lane & 15);  // this lane's step as a column
     const int64_t tn = t0 + n;
@@ -244,12 +228,8 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
     f32x4 dq_all[2 * KS], dk_all[2 * KS];
 #pragma unroll
     for (int t = 0; t < 2 * KS; ++t) dq_all[t] = dk_all[t] = zero4();
-    if (t0 < len) {
-        const KeyCopy<T, KS, 4> keys(p, b, hk, len, wave, lane);
-        keys(s_k, p.kr, c);
-        keys(s_q, p.qr, c);
-        wait_copies();  // of this wave; the others' behind the first barrier
-    }
+    const KeyCopy<T, KS, 4> keys(p, b, hk, len, wave, lane);
+    const int slabs = static_cast<int>(p.VP / 32);
     for (int64_t hv = hk * group; hv < (hk + 1) * group; ++hv) {
         const int64_t gate = (b * p.L + t0 + lane) * p.Hv + hv;
         if (t0 >= len) {
@@ -273,99 +253,81 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
             }
             s_g[lane] = G;
         }
-        __syncthreads();
         const float ga_n = vec[n], w_n = vec[kC + n], be_n = vec[2 * kC + n];
         f32x4 D1[2 * KS], D2[2 * KS], D3[2 * KS], A1[4], A2[4], B1[4], B2[4];
 #pragma unroll
         for (int t = 0; t < 2 * KS; ++t) D1[t] = D2[t] = D3[t] = zero4();
 #pragma unroll
         for (int t = 0; t < 4; ++t) A1[t] = A2[t] = B1[t] = B2[t] = zero4();
-        float dbeta = 0.f, bound = 0.f;
-        const T* dyh = static_cast<const T*>(gp.dy) + (b * p.L * p.Hv + hv) * p.V;
-        const float *dr = gp.dr + bhc * kC * VP, *news = p.news + bhc * kC * VP;
-        const float *Sa = p.states + bhc * (32 * KS) * VP, *Sb = gp.after + bhc * (32 * KS) * VP;
-        for (int64_t v0 = 8 * q; v0 < VP; v0 += 32) {
-            float x[8], y[8];
-            Planes<kN> On;
-            Planes<kO> En, Un;
-            row8<T>(dyh + tn * p.Hv * p.V, v0, p.V, tn < len, gp.vec_dy, x);
-            split8<kN>(x, On);
-            load8(dr + n * VP + v0, x);
-            load8(news + n * VP + v0, y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dbeta += x[j] * y[j];
-                x[j] *= be_n;
-                y[j] *= be_n;
-            }
-            split8<kO>(x, En);
-            split8<kO>(y, Un);
+        float bound = 0.f;
+        for (int sl = 0; sl < slabs; ++sl) {
+            barrier();
+            stage_block<Sl::kElements / kFrag, 4>(s_buf, p.slab + (bhc * slabs + sl) * Sl::kElements, wave, lane);
+            wait_copies();
+            barrier();
+            const uint16_t *sE = s_buf + Sl::kE, *sR = s_buf + Sl::kDr, *sY = s_buf + Sl::kDy;
+            const Planes<kN> On = col_frag<kN, 64, 32>(sY, wave, 0, lane);
+            const Planes<kO> Rn = col_frag<kO, 64, 32>(sR, wave, 0, lane);
+            const Planes<kO> En = col_frag<kO, 64, 32>(sE, wave, 0, lane);
 #pragma unroll
             for (int t = 0; t < 2 * KS; ++t) {
-                const int64_t at = static_cast<int64_t>(tile_row(t, lane & 15)) * VP + v0;
-                Planes<kO> a, d;
-                load8(Sa + at, x);
-                load8(Sb + at, y);
+                const Planes<kO> a = col_frag<kO, kPitch, 32>(s_buf + Sl::kS, t, 0, lane);
+                const Planes<kO> d = col_frag<kO, kPitch, 32>(s_buf + Sl::kDs, t, 0, lane);
                 if ((t & 3) == wave)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) bound += x[j] * y[j];
-                split8<kO>(x, a);
-                split8<kO>(y, d);
+                    for (int j = 0; j < 8; ++j) bound += plane_sum(a, j) * plane_sum(d, j);
                 D1[t] = mma<kO>(a, On, D1[t]);
-                D2[t] = mma<kO>(a, En, D2[t]);
-                D3[t] = mma<kO>(d, Un, D3[t]);
+                D2[t] = mma<kO>(a, Rn, D2[t]);
+                D3[t] = mma<kO>(d, En, D3[t]);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int m = tile_row(t, lane & 15);
-                const float be_m = vec[2 * kC + m];
                 if (t / 2 <= wave / 2) {  // rows j not behind this wave's steps
-                    Planes<kO> u;
-                    load8(news + m * VP + v0, x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] *= be_m;
-                    split8<kO>(x, u);
-                    A1[t] = mma<kO>(u, On, A1[t]);
-                    A2[t] = mma<kO>(u, En, A2[t]);
+                    const Planes<kO> e = col_frag<kO, 64, 32>(sE, t, 0, lane);
+                    A1[t] = mma<kO>(e, On, A1[t]);
+                    A2[t] = mma<kO>(e, Rn, A2[t]);
                 }
                 if (t / 2 >= wave / 2) {  // rows i not before them
-                    Planes<kN> o;
-                    Planes<kO> e;
-                    row8<T>(dyh + (t0 + m) * p.Hv * p.V, v0, p.V, t0 + m < len, gp.vec_dy, x);
-                    split8<kN>(x, o);
-                    load8(dr + m * VP + v0, x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] *= be_m;
-                    split8<kO>(x, e);
-                    B1[t] = mma<kO>(o, Un, B1[t]);
-                    B2[t] = mma<kO>(e, Un, B2[t]);
+                    const Planes<kN> o = col_frag<kN, 64, 32>(sY, t, 0, lane);
+                    const Planes<kO> r = col_frag<kO, 64, 32>(sR, t, 0, lane);
+                    B1[t] = mma<kO>(o, En, B1[t]);
+                    B2[t] = mma<kO>(r, En, B2[t]);
                 }
             }
         }
-        // decays and masks, then the blocks as right operands: k step s = tiles 2s, 2s + 1
+        barrier();
+        keys(s_k, p.kr, c);
+        keys(s_q, p.qr, c);
+        // decays and masks, then the blocks as right operands: k step s = tiles 2s, 2s + 1.
+        // dbeta is the diagonal of dR E^^T.
         Planes<kO> a1[2], a2[2], b1[2], b2[2];
+        float dbeta = 0.f;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            float xa1[8], xa2[8], xb1[8], xb2[8];
+            float xa1[8], xa2[8], xb1[8], xb2[8], be[8];
+            load8(vec + 2 * kC + 32 * s + 8 * q, be);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int t = 2 * s + (j >> 2), m = 32 * s + 8 * q + j;
-                const float up = m <= n ? expf(static_cast<float>(s_g[n] - s_g[m])) : 0.f;
-                const float dn = m >= n ? expf(static_cast<float>(s_g[m] - s_g[n])) : 0.f;
-                xa1[j] = m <= n ? A1[t][j & 3] * up : 0.f;
-                xa2[j] = m < n ? A2[t][j & 3] * up : 0.f;
-                xb1[j] = m >= n ? B1[t][j & 3] * dn * p.scale : 0.f;
-                xb2[j] = m > n ? -B2[t][j & 3] * dn : 0.f;
+                const float d = static_cast<float>(m <= n ? s_g[n] - s_g[m] : s_g[m] - s_g[n]);
+                const float e = expf(d);
+                if (m == n) dbeta = A2[t][j & 3];
+                xa1[j] = m <= n ? A1[t][j & 3] * (e * be[j]) : 0.f;
+                xa2[j] = m < n ? A2[t][j & 3] * (e * be[j] * be_n) : 0.f;
+                xb1[j] = m >= n ? B1[t][j & 3] * (e * be_n * p.scale) : 0.f;
+                xb2[j] = m > n ? B2[t][j & 3] * (-e * be[j] * be_n) : 0.f;
             }
             split8<kO>(xa1, a1[s]);
             split8<kO>(xa2, a2[s]);
             split8<kO>(xb1, b1[s]);
             split8<kO>(xb2, b2[s]);
         }
+        wait_copies();
+        barrier();
         float dG = 0.f, kover = 0.f;
 #pragma unroll
         for (int t = 0; t < 2 * KS; ++t) {
-            f32x4 gq = D1[t] * ga_n, row = D2[t] * ga_n, col = D3[t] * w_n;
+            f32x4 gq = D1[t] * ga_n, row = D2[t] * (ga_n * be_n), col = D3[t] * (w_n * be_n);
             const Planes<kN> kr = row_frag<kN, kPitch>(s_k, wave, t >> 1, lane);
             const Planes<kN> qr = row_frag<kN, kPitch>(s_q, wave, t >> 1, lane);
 #pragma unroll
@@ -385,8 +347,8 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
                 dG += plane_sum(qr, 4 * (t & 1) + r) * gq[r];
                 dG -= plane_sum(kr, 4 * (t & 1) + r) * (row[r] + col[r]);
             }
-            dq_all[t] += gq;
-            dk_all[t] += col - row;
+            dq_all[t] = GROUPED ? dq_all[t] + gq : gq;
+            dk_all[t] = GROUPED ? dk_all[t] + (col - row) : col - row;
         }
         dG = sum_quarters(dG);
         dbeta = sum_quarters(dbeta);
@@ -413,7 +375,6 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(GradParams gp) {
                 Elem<T>::store(db, gate, in ? s_db[lane] : 0.f);
             }
         }
-        __syncthreads();
     }
     if (tn < p.L) {
         const int64_t at = ((b * p.L + tn) * p.Hk + hk) * p.K;
