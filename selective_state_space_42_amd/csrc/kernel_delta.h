@@ -126,6 +126,20 @@ __device__ __forceinline__ f32x4 mma(const Planes<NA>& a, const Planes<NB>& b, f
     return c;
 }
 
+// c[t] += a[t] b for NT tiles, in turn: an instruction's result is ready for the
+// next one on the same accumulator only after two instructions' time
+template <int LIM, int NT, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(const Planes<NA> (&a)[NT], const Planes<NB>& b, f32x4* c) {
+#pragma unroll
+    for (int d = LIM - 1; d >= 0; --d)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (d - i >= 0 && d - i < NB) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) c[t] = mfma(a[t].p[i], b.p[d - i], c[t]);
+            }
+}
+
 // fragment f of each plane, planes `stride` fragments apart
 template <int N>
 __device__ __forceinline__ Planes<N> frag(const uint16_t* base, int f, int stride, int lane) {
@@ -603,6 +617,7 @@ template <typename T, int KS, bool OUT, int NW, int NBUF>
 __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
     constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
     constexpr int kUnits = OUT ? block_units<T, false>() : 1 + kSplit;
+    constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;  // of the state, at a time
     using St = Stage<T, KS, kUnits, OUT>;
     using Blk = Block<!OUT>;
     extern __shared__ __align__(16) uint16_t smem[];
@@ -678,17 +693,19 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
             split8<3>(x, Sp[s]);
             if constexpr (!OUT) put_planes<kO, kPitch>(ws, slab_off, slab_row, Sl::kS, 4 * s + q, Sp[s]);
         }
-        // E^ and U, two row tiles (32 steps) at a time: lane's steps 32 s + 8 q + 0 .. 7
+        // E^ and U; this lane's steps are 32 s + 8 q + 0 .. 7
+        f32x4 acc[4] = {zero4(), zero4(), zero4(), zero4()};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            Planes<kN> a[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t] = row_frag<kN, kPitch>(st + St::kK, t, s, lane);
+            mma_tiles<3>(a, Sp[s], acc);
+        }
         float E[2][8], be[2][8];
         Planes<3> Y[2];
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
-            f32x4 ks[2] = {zero4(), zero4()};
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    ks[t] = mma<3>(row_frag<kN, kPitch>(st + St::kK, 2 * s2 + t, s, lane), Sp[s], ks[t]);
             float ga[8], x[8];
             load8(vec + 32 * s2 + 8 * q, ga);
             load8(vec + 2 * kC + 32 * s2 + 8 * q, be[s2]);
@@ -703,10 +720,21 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                E[s2][j] = x[j] - ga[j] * ks[j >> 2][j & 3];
+                E[s2][j] = x[j] - ga[j] * acc[2 * s2 + (j >> 2)][j & 3];
                 x[j] = be[s2][j] * E[s2][j];
             }
             split8<3>(x, Y[s2]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[t] = zero4();
+        {
+            Planes<3> a[4], a2[2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t] = frag<3>(xf, tri_lower(t, 0), kTri, lane);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) a2[t] = frag<3>(xf, tri_lower(2 + t, 1), kTri, lane);
+            mma_tiles<3>(a, Y[0], acc);
+            mma_tiles<3>(a2, Y[1], acc + 2);
         }
         Planes<kO> U[2];
         Planes<3> W[2];
@@ -715,50 +743,57 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
             float x[8], w[8];
             load8(vec + kC + 32 * s2 + 8 * q, w);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                f32x4 a = zero4();
-#pragma unroll
-                for (int s = 0; s <= s2; ++s)
-                    a = mma<3>(frag<3>(xf, tri_lower(2 * s2 + t, s), kTri, lane), Y[s], a);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float e = E[s2][4 * t + r] - a[r], u = be[s2][4 * t + r] * e;
-                    x[4 * t + r] = OUT ? u : e;
-                    w[4 * t + r] *= u;
-                }
+            for (int j = 0; j < 8; ++j) {
+                const float e = E[s2][j] - acc[2 * s2 + (j >> 2)][j & 3], u = be[s2][j] * e;
+                x[j] = OUT ? u : e;
+                w[j] *= u;
             }
             split8<kO>(x, U[s2]);  // E^ without beta where it is kept for the gradients
             if constexpr (!OUT) put_planes<kO, 64>(ws, slab_off, slab_row, Sl::kE, 4 * s2 + q, U[s2]);
             split8<3>(w, W[s2]);
         }
-        if constexpr (OUT) {
-#pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2) {
-                float ga[8];
-                load8(vec + 32 * s2 + 8 * q, ga);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    f32x4 a = zero4();
-#pragma unroll
-                    for (int s = 0; s < KS; ++s)
-                        a = mma<kO>(row_frag<kN, kPitch>(st + St::kQ, 2 * s2 + t, s, lane), Sp[s], a);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) a[r] *= ga[4 * t + r] * p.scale;
-#pragma unroll
-                    for (int s = 0; s <= s2; ++s)
-                        a = mma<kO>(frag<kO>(pf, tri_lower(2 * s2 + t, s), kTri, lane), U[s], a);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) out[s2][4 * t + r] = a[r];
-                }
-            }
-        }
+        // the state first: the next chunk waits for it
         const float end = vec[kC - 1];
 #pragma unroll
-        for (int t = 0; t < 2 * KS; ++t) {
-            f32x4 a = S[t] * end;
+        for (int t = 0; t < 2 * KS; ++t) S[t] *= end;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) a = mma<3>(col_frag<kN, kPitch>(st + St::kK, t, s, lane), W[s], a);
-            S[t] = a;
+        for (int t0 = 0; t0 < 2 * KS; t0 += kTiles) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                Planes<kN> a[kTiles];
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) a[t] = col_frag<kN, kPitch>(st + St::kK, t0 + t, s, lane);
+                mma_tiles<3>(a, W[s], S + t0);
+            }
+        }
+        if constexpr (OUT) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t] = zero4();
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                Planes<kN> a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = row_frag<kN, kPitch>(st + St::kQ, t, s, lane);
+                mma_tiles<kO>(a, Sp[s], acc);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                float ga[8];
+                load8(vec + 32 * s + 8 * q, ga);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[2 * s + (j >> 2)][j & 3] *= ga[j] * p.scale;
+            }
+            Planes<kO> a[4], a2[2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t] = frag<kO>(pf, tri_lower(t, 0), kTri, lane);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) a2[t] = frag<kO>(pf, tri_lower(2 + t, 1), kTri, lane);
+            mma_tiles<kO>(a, U[0], acc);
+            mma_tiles<kO>(a2, U[1], acc + 2);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) out[s][j] = acc[2 * s + (j >> 2)][j & 3];
         }
     }
     if (OUT && chunks > 0) put_out(chunks - 1);

@@ -36,6 +36,7 @@ struct GradParams {
 template <typename T, int KS, int NW, int NBUF>
 __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp) {
     constexpr int kN = PlanesOf<T>::kIn, kPitch = pitch_of<KS>(), kUnits = 2 * kSplit + 1;
+    constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;
     using St = Stage<T, KS, kUnits, true>;
     using Blk = Block<true>;
     extern __shared__ __align__(16) uint16_t smem[];
@@ -126,47 +127,55 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
             for (int j = 0; j < 8; ++j) x[j] *= ga[s][j] * p.scale;
             split8<3>(x, gO[s]);
         }
+        f32x4 acc[4] = {zero4(), zero4(), zero4(), zero4()};
 #pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2) {
-            float w[8], x[8];
-            load8(vec + kC + 32 * s2 + 8 * q, w);
+        for (int s = 0; s < KS; ++s) {
+            Planes<kN> a[4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                f32x4 a = zero4();
-#pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    a = mma<3>(row_frag<kN, kPitch>(st + St::kK, 2 * s2 + t, s, lane), Sp[s], a);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) a[r] *= w[4 * t + r];
-#pragma unroll
-                for (int s = s2; s < 2; ++s)
-                    a = mma<3>(frag<3>(ptf, tri_upper(2 * s2 + t, s), kTri, lane), dO[s], a);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    du[s2][4 * t + r] = a[r];
-                    x[4 * t + r] = be[s2][4 * t + r] * a[r];
-                }
-            }
-            split8<3>(x, Y[s2]);
+            for (int t = 0; t < 4; ++t) a[t] = row_frag<kN, kPitch>(st + St::kK, t, s, lane);
+            mma_tiles<3>(a, Sp[s], acc);
         }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float w[8];
+            load8(vec + kC + 32 * s + 8 * q, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[2 * s + (j >> 2)][j & 3] *= w[j];
+        }
+        // upper triangles: steps 32 .. 63 reach all four row tiles, 0 .. 31 the first two
+        const auto upper = [&](const uint16_t* f, const auto& first, const auto& second) {
+            Planes<3> a[4], a2[2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[t] = frag<3>(f, tri_upper(t, 1), kTri, lane);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) a2[t] = frag<3>(f, tri_upper(t, 0), kTri, lane);
+            mma_tiles<3>(a, second, acc);
+            mma_tiles<3>(a2, first, acc);
+        };
+        upper(ptf, dO[0], dO[1]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                du[s][j] = acc[2 * s + (j >> 2)][j & 3];
+                x[j] = be[s][j] * du[s][j];
+            }
+            split8<3>(x, Y[s]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[t] = zero4();
+        upper(xtf, Y[0], Y[1]);
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
             float x[8], dr[8];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                f32x4 a = zero4();
-#pragma unroll
-                for (int s = s2; s < 2; ++s)
-                    a = mma<3>(frag<3>(xtf, tri_upper(2 * s2 + t, s), kTri, lane), Y[s], a);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = 4 * t + r, i = 32 * s2 + 8 * q + j;
-                    dr[j] = du[s2][j] - a[r];
-                    const float de = be[s2][j] * dr[j];
-                    Buf<T>::store(wv, yoff + (32 * s2 + j) * ystep,
-                                  t0 + i < len ? de : 0.f);
-                    x[j] = -ga[s2][j] * de;
-                }
+            for (int j = 0; j < 8; ++j) {
+                const int i = 32 * s2 + 8 * q + j;
+                dr[j] = du[s2][j] - acc[2 * s2 + (j >> 2)][j & 3];
+                const float de = be[s2][j] * dr[j];
+                Buf<T>::store(wv, yoff + (32 * s2 + j) * ystep, t0 + i < len ? de : 0.f);
+                x[j] = -ga[s2][j] * de;
             }
             split8<3>(x, gE[s2]);
             Planes<Sl::kO> R;
@@ -175,17 +184,33 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
         }
         const float end = vec[kC - 1];
 #pragma unroll
-        for (int t = 0; t < 2 * KS; ++t) {
-            f32x4 a = S[t] * end;
+        for (int t = 0; t < 2 * KS; ++t) S[t] *= end;
+#pragma unroll
+        for (int t1 = 0; t1 < 2 * KS; t1 += kTiles) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                a = mma<3>(col_frag<kN, kPitch>(st + St::kQ, t, s, lane), gO[s], a);
-                a = mma<3>(col_frag<kN, kPitch>(st + St::kK, t, s, lane), gE[s], a);
+                Planes<kN> a[kTiles];
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) a[t] = col_frag<kN, kPitch>(st + St::kQ, t1 + t, s, lane);
+                mma_tiles<3>(a, gO[s], S + t1);
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) a[t] = col_frag<kN, kPitch>(st + St::kK, t1 + t, s, lane);
+                mma_tiles<3>(a, gE[s], S + t1);
             }
-            S[t] = a;
         }
     }
     if (gp.dh0) store_state<KS>(gp.dh0 + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
+}
+
+// 8 neighbours at a 16-byte boundary
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+    Planes<1> o;
+    split8<1>(x, o);
+    *reinterpret_cast<bf16x8*>(p) = o.p[0];
 }
 
 template <int N>
@@ -270,28 +295,41 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
             const Planes<kO> Rn = col_frag<kO, 64, 32>(sR, wave, 0, lane);
             const Planes<kO> En = col_frag<kO, 64, 32>(sE, wave, 0, lane);
 #pragma unroll
-            for (int t = 0; t < 2 * KS; ++t) {
-                const Planes<kO> a = col_frag<kO, kPitch, 32>(s_buf + Sl::kS, t, 0, lane);
-                const Planes<kO> d = col_frag<kO, kPitch, 32>(s_buf + Sl::kDs, t, 0, lane);
-                if ((t & 3) == wave)
+            for (int t = 0; t < 2 * KS; t += 2) {
+                Planes<kO> a[2], d[2];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) bound += plane_sum(a, j) * plane_sum(d, j);
-                D1[t] = mma<kO>(a, On, D1[t]);
-                D2[t] = mma<kO>(a, Rn, D2[t]);
-                D3[t] = mma<kO>(d, En, D3[t]);
+                for (int i = 0; i < 2; ++i) {
+                    a[i] = col_frag<kO, kPitch, 32>(s_buf + Sl::kS, t + i, 0, lane);
+                    d[i] = col_frag<kO, kPitch, 32>(s_buf + Sl::kDs, t + i, 0, lane);
+                }
+                mma_tiles<kO>(a, On, D1 + t);
+                mma_tiles<kO>(a, Rn, D2 + t);
+                mma_tiles<kO>(d, En, D3 + t);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (((t + i) & 3) == wave)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) bound += plane_sum(a[i], j) * plane_sum(d[i], j);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < 4; t += 2) {
                 if (t / 2 <= wave / 2) {  // rows j not behind this wave's steps
-                    const Planes<kO> e = col_frag<kO, 64, 32>(sE, t, 0, lane);
-                    A1[t] = mma<kO>(e, On, A1[t]);
-                    A2[t] = mma<kO>(e, Rn, A2[t]);
+                    Planes<kO> e[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) e[i] = col_frag<kO, 64, 32>(sE, t + i, 0, lane);
+                    mma_tiles<kO>(e, On, A1 + t);
+                    mma_tiles<kO>(e, Rn, A2 + t);
                 }
                 if (t / 2 >= wave / 2) {  // rows i not before them
-                    const Planes<kN> o = col_frag<kN, 64, 32>(sY, t, 0, lane);
-                    const Planes<kO> r = col_frag<kO, 64, 32>(sR, t, 0, lane);
-                    B1[t] = mma<kO>(o, En, B1[t]);
-                    B2[t] = mma<kO>(r, En, B2[t]);
+                    Planes<kN> o[2];
+                    Planes<kO> r[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        o[i] = col_frag<kN, 64, 32>(sY, t + i, 0, lane);
+                        r[i] = col_frag<kO, 64, 32>(sR, t + i, 0, lane);
+                    }
+                    mma_tiles<kO>(o, En, B1 + t);
+                    mma_tiles<kO>(r, En, B2 + t);
                 }
             }
         }
@@ -310,7 +348,8 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
             for (int j = 0; j < 8; ++j) {
                 const int t = 2 * s + (j >> 2), m = 32 * s + 8 * q + j;
                 const float d = static_cast<float>(m <= n ? s_g[n] - s_g[m] : s_g[m] - s_g[n]);
-                const float e = expf(d);
+                // 16-bit planes follow, except in fp32
+                const float e = sizeof(T) == 4 ? expf(d) : __builtin_amdgcn_exp2f(d * kLog2e);
                 if (m == n) dbeta = A2[t][j & 3];
                 xa1[j] = m <= n ? A1[t][j & 3] * (e * be[j]) : 0.f;
                 xa2[j] = m < n ? A2[t][j & 3] * (e * be[j] * be_n) : 0.f;
@@ -326,29 +365,42 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
         barrier();
         float dG = 0.f, kover = 0.f;
 #pragma unroll
-        for (int t = 0; t < 2 * KS; ++t) {
-            f32x4 gq = D1[t] * ga_n, row = D2[t] * (ga_n * be_n), col = D3[t] * (w_n * be_n);
+        for (int t = 0; t < 2 * KS; t += 2) {
             const Planes<kN> kr = row_frag<kN, kPitch>(s_k, wave, t >> 1, lane);
             const Planes<kN> qr = row_frag<kN, kPitch>(s_q, wave, t >> 1, lane);
+            f32x4 gq[2], row[2], col[2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) kover += plane_sum(kr, 4 * (t & 1) + r) * col[r];
+            for (int i = 0; i < 2; ++i) {
+                gq[i] = D1[t + i] * ga_n;
+                row[i] = D2[t + i] * (ga_n * be_n);
+                col[i] = D3[t + i] * (w_n * be_n);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) kover += plane_sum(kr, 4 * i + r) * col[i][r];
+            }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const Planes<kN> kt = col_frag<kN, kPitch>(s_k, t, s, lane);
-                const Planes<kN> qt = col_frag<kN, kPitch>(s_q, t, s, lane);
-                gq = mma<kO>(kt, a1[s], gq);
-                row = mma<kO>(kt, a2[s], row);
-                col = mma<kO>(qt, b1[s], col);
-                col = mma<kO>(kt, b2[s], col);
-            }
-            gq *= p.scale;
+                Planes<kN> kt[2], qt[2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                dG += plane_sum(qr, 4 * (t & 1) + r) * gq[r];
-                dG -= plane_sum(kr, 4 * (t & 1) + r) * (row[r] + col[r]);
+                for (int i = 0; i < 2; ++i) {
+                    kt[i] = col_frag<kN, kPitch>(s_k, t + i, s, lane);
+                    qt[i] = col_frag<kN, kPitch>(s_q, t + i, s, lane);
+                }
+                mma_tiles<kO>(kt, a1[s], gq);
+                mma_tiles<kO>(kt, a2[s], row);
+                mma_tiles<kO>(qt, b1[s], col);
+                mma_tiles<kO>(kt, b2[s], col);
             }
-            dq_all[t] = GROUPED ? dq_all[t] + gq : gq;
-            dk_all[t] = GROUPED ? dk_all[t] + (col - row) : col - row;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                gq[i] *= p.scale;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    dG += plane_sum(qr, 4 * i + r) * gq[i][r];
+                    dG -= plane_sum(kr, 4 * i + r) * (row[i][r] + col[i][r]);
+                }
+                dq_all[t + i] = GROUPED ? dq_all[t + i] + gq[i] : gq[i];
+                dk_all[t + i] = GROUPED ? dk_all[t + i] + (col[i] - row[i]) : col[i] - row[i];
+            }
         }
         dG = sum_quarters(dG);
         dbeta = sum_quarters(dbeta);
@@ -378,16 +430,32 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
     }
     if (tn < p.L) {
         const int64_t at = ((b * p.L + tn) * p.Hk + hk) * p.K;
+        const bool live = tn < len;
+        const bool pieces = p.K % 8 == 0 && reinterpret_cast<uintptr_t>(dq) % 16 == 0 &&
+                            reinterpret_cast<uintptr_t>(dk) % 16 == 0;
 #pragma unroll
-        for (int t = 0; t < 2 * KS; ++t)
+        for (int s = 0; s < KS; ++s) {
+            const int e = 32 * s + 8 * q;
+            float x[8], y[8];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int e = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r;
-                if (e < p.K) {
-                    Elem<T>::store(dq, at + e, tn < len ? dq_all[t][r] : 0.f);
-                    Elem<T>::store(dk, at + e, tn < len ? dk_all[t][r] : 0.f);
-                }
+            for (int j = 0; j < 8; ++j) {
+                x[j] = live ? dq_all[2 * s + (j >> 2)][j & 3] : 0.f;
+                y[j] = live ? dk_all[2 * s + (j >> 2)][j & 3] : 0.f;
             }
+            if (pieces) {
+                if (e < p.K) {
+                    store8(dq + at + e, x);
+                    store8(dk + at + e, y);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e + j < p.K) {
+                    Elem<T>::store(dq, at + e + j, x[j]);
+                    Elem<T>::store(dk, at + e + j, y[j]);
+                }
+        }
     }
 }
 
