@@ -83,7 +83,13 @@ void sweep(Params p, hipStream_t s) {
     constexpr int lds = NBUF * Stage<T, KS, units, OUT>::kElements * 2;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     p.nV = ((OUT ? p.V : p.VP) + 16 * NW - 1) / (16 * NW);
-    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, OUT, NW, NBUF>), grid(p.B * p.Hv * p.nV), dim3(64 * NW), lds, s, p);
+    const dim3 g = grid(p.B * p.Hv * p.nV), block(64 * NW);
+    if constexpr (sizeof(T) == 2)
+        if (p.vec_v) {
+            hipLaunchKernelGGL((delta_chunk_kernel<T, KS, OUT, NW, NBUF, true>), g, block, lds, s, p);
+            return;
+        }
+    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, OUT, NW, NBUF, false>), g, block, lds, s, p);
 }
 
 template <typename T, int KS, int NW, int NBUF>
@@ -91,8 +97,13 @@ void adjoint(GradParams g, hipStream_t s) {
     constexpr int lds = NBUF * Stage<T, KS, 2 * kSplit + 1, true>::kElements * 2;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     g.f.nV = (g.f.VP + 16 * NW - 1) / (16 * NW);
-    hipLaunchKernelGGL((delta_adjoint_kernel<T, KS, NW, NBUF>), grid(g.f.B * g.f.Hv * g.f.nV), dim3(64 * NW), lds, s,
-                       g);
+    const dim3 gr = grid(g.f.B * g.f.Hv * g.f.nV), block(64 * NW);
+    if constexpr (sizeof(T) == 2)
+        if (g.vec_dy) {
+            hipLaunchKernelGGL((delta_adjoint_kernel<T, KS, NW, NBUF, true>), gr, block, lds, s, g);
+            return;
+        }
+    hipLaunchKernelGGL((delta_adjoint_kernel<T, KS, NW, NBUF, false>), gr, block, lds, s, g);
 }
 
 template <typename T, int KS, bool BWD>
@@ -199,6 +210,7 @@ int ssm_delta_fwd(const ssm_delta_desc_t* d, const void* q, const void* k, const
     Params p = params(d, o, false, workspace, q, k);
     p.v = v; p.g = g; p.beta = beta; p.h0 = h0; p.lengths = lengths; p.y = y; p.h_last = h_last;
     p.vec_v = d->dvalue * io_size(d) % 16 == 0 && ssm::aligned(v, 16);
+    p.vec_y = d->dvalue % 4 == 0 && ssm::aligned(y, 4 * io_size(d));
     return by_size<Fwd>(d, p, static_cast<hipStream_t>(stream));
 }
 

@@ -65,7 +65,7 @@ struct Params {
     int64_t B, L, Hk, Hv, K, V, nC;
     int64_t nV, VP;                 // column groups of a workgroup, and the state's columns in all
     float scale;
-    int32_t packed, vec_v;          // kr, qr are packed; rows of v (and dy) move in 16-byte pieces
+    int32_t packed, vec_v, vec_y;   // kr, qr are packed; rows of v move in 16-byte pieces, those of y in 4 elements
 };
 
 // A chunk's block: (backward: X^T, 18 fragments, P^T, 18) e^G, e^{G_63 - G} and
@@ -137,6 +137,19 @@ __device__ __forceinline__ void mma_tiles(const Planes<NA> (&a)[NT], const Plane
             if (d - i >= 0 && d - i < NB) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) c[t] = mfma(a[t].p[i], b.p[d - i], c[t]);
+            }
+}
+
+// c[t] += b a[t]: the same with `a` on the right, for the transposed result
+template <int LIM, int NT, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(const Planes<NB>& b, const Planes<NA> (&a)[NT], f32x4* c) {
+#pragma unroll
+    for (int d = LIM - 1; d >= 0; --d)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (d - i >= 0 && d - i < NB) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) c[t] = mfma(b.p[d - i], a[t].p[i], c[t]);
             }
 }
 
@@ -573,6 +586,35 @@ __device__ __forceinline__ void store_state(float* h, int64_t K, bool ok, int la
     }
 }
 
+// Column `col` (-1: none) of a chunk's 64 rows of `src`: this lane's steps
+// 32 s + 8 (l / 16) + j, zeros from row `left` on.  TILE: from the staged tile.
+template <typename T, bool TILE>
+__device__ __forceinline__ void column_values(float (&x)[2][8], const uint16_t* tile, const T* src, int64_t left,
+                                              uint32_t step, int64_t col, int wave, int lane) {
+    if constexpr (TILE) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) col_values(tile, s, 16 * wave, lane, x[s]);
+    } else {
+        const rsrc_t w = buffer(src, static_cast<uint32_t>(left < 64 ? left : 64) * step);
+        const uint32_t off = col < 0 ? kNowhere : 8 * (lane >> 4) * step + static_cast<uint32_t>(col * sizeof(T));
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[s][j] = Buf<T>::load(w, off + (32 * s + j) * step);
+    }
+}
+
+// four neighbours at a boundary of their size
+template <typename T>
+__device__ __forceinline__ void put4(rsrc_t w, uint32_t off, f32x4 x) {
+    if constexpr (sizeof(T) == 4) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), w, off, 0, 0);
+    } else {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, w, off, 0, 0);
+    }
+}
+
 // What the sweeps of the backward pass leave for delta_grad_kernel: for each
 // (chunk, value head) and 32 columns v, in bf16 planes, tiles with a row for
 // each v (swizzled as in LDS): the state entering the chunk, the gradient of the one
@@ -586,8 +628,6 @@ struct Slab {
     static constexpr int kElements = kDy + kN * 32 * 64;
 };
 
-typedef uint32_t store4 __attribute__((ext_vector_type(4)));
-
 // planes of 8 neighbours (piece `piece`) of row v of a slab's tile at element `at`
 template <int N, int PITCH, int M>
 __device__ __forceinline__ void put_planes(rsrc_t w, uint32_t slab_off, int v, int at, int piece, const Planes<M>& x) {
@@ -595,7 +635,7 @@ __device__ __forceinline__ void put_planes(rsrc_t w, uint32_t slab_off, int v, i
 #pragma unroll
     for (int n = 0; n < N; ++n)
         __builtin_amdgcn_raw_buffer_store_b128(
-            __builtin_bit_cast(store4, x.p[n]), w,
+            __builtin_bit_cast(u32x4, x.p[n]), w,
             slab_off + 2 * (at + (n * 32 + v) * PITCH + 8 * (piece ^ swizzle<PITCH>(v))), 0, 0);
 }
 
@@ -612,9 +652,10 @@ struct Stage {
 // waves (neighbouring columns) sharing what is staged in LDS.  With two
 // buffers the next chunk's copies run under this chunk's products.
 // OUT: writes y and h_last (the forward); else the states entering each chunk
-// and E^ (what the gradients read).
-template <typename T, int KS, bool OUT, int NW, int NBUF>
-__global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
+// and E^ (what the gradients read).  VT: values are staged too (bf16 rows of
+// whole 16-byte pieces).
+template <typename T, int KS, bool OUT, int NW, int NBUF, bool VT>
+__global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
     constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
     constexpr int kUnits = OUT ? block_units<T, false>() : 1 + kSplit;
     constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;  // of the state, at a time
@@ -630,7 +671,8 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
     const T* v = static_cast<const T*>(p.v) + (b * p.L * p.Hv + h) * p.V;
     T* y = static_cast<T*>(p.y) + (b * p.L * p.Hv + h) * p.V;
     const int64_t vstride = p.Hv * p.V;
-    const bool vtile = sizeof(T) == 2 && p.vec_v;
+    static_assert(!VT || sizeof(T) == 2, "a tile of values is one bf16 plane");
+    const uint32_t ystep = static_cast<uint32_t>(vstride * sizeof(T));
 
     const KeyCopy<T, KS, NW> keys(p, b, hk, len, wave, lane);
     const int64_t cols = p.V - col0;
@@ -641,7 +683,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
         stage_block<kUnits, NW>(st, blk + Blk::kVec * kFrag, wave, lane);
         keys(st + St::kK, p.kr, c);
         if constexpr (OUT) keys(st + St::kQ, p.qr, c);
-        if (vtile) {
+        if constexpr (VT) {
             const int64_t left = len - c * kC;
             values(st + St::kV, reinterpret_cast<const uint16_t*>(v) + c * kC * vstride + col0,
                    left < 64 ? static_cast<int>(left) : 64);
@@ -650,17 +692,24 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
 
     f32x4 S[2 * KS];
     load_state<KS>(p.h0 ? p.h0 + (bh * p.V + (ok ? col : 0)) * p.K : nullptr, p.K, ok, lane, S);
-    float out[2][8];  // y of the chunk before, stored under this chunk's products
-    const uint32_t ystep = static_cast<uint32_t>(vstride * sizeof(T));
-    const uint32_t yoff = ok ? 8 * q * ystep + static_cast<uint32_t>(col * sizeof(T)) : kNowhere;
+    // y^T of the chunk before, stored under this chunk's products: this lane's
+    // step of tile t, columns 4 q + 0 .. 3 of the wave's
+    f32x4 out[4];
+    const uint32_t ycol = static_cast<uint32_t>(col0 + 16 * wave + 4 * q);
     const auto put_out = [&](int64_t c) {  // rows behind the length are outside the window
         const int64_t left = len - c * kC;
         const rsrc_t w = buffer(y + c * kC * vstride, static_cast<uint32_t>(left < 64 ? left : 64) * ystep);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t off = tile_row(t, lane & 15) * ystep + ycol * sizeof(T);
+            if (p.vec_y) {
+                put4<T>(w, ycol < p.V ? off : kNowhere, out[t]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                Buf<T>::store(w, yoff + (32 * s + j) * ystep, out[s][j]);
+                for (int r = 0; r < 4; ++r)
+                    Buf<T>::store(w, ycol + r < p.V ? off + r * sizeof(T) : kNowhere, out[t][r]);
+            }
+        }
     };
     using Sl = Slab<T, KS>;
     const uint32_t slab_off = col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
@@ -681,8 +730,10 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
         if (OUT && c > 0) put_out(c - 1);
         const uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
         const float* vec = reinterpret_cast<const float*>(st);
+        float v8[2][8];
+        column_values<T, VT>(v8, st + St::kV, v + c * kC * vstride, len - c * kC, ystep, ok ? col : -1, wave, lane);
         const uint16_t *xf = st + kFrag, *pf = st + (1 + kSplit) * kFrag;
-        const int64_t t0 = c * kC, bhc = bh * p.nC + c;
+        const int64_t bhc = bh * p.nC + c;
         const rsrc_t ws = buffer(OUT ? nullptr : p.slab + bhc * (slab_bytes / 2), slab_bytes);
         Planes<3> Sp[KS];
 #pragma unroll
@@ -709,18 +760,9 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
             float ga[8], x[8];
             load8(vec + 32 * s2 + 8 * q, ga);
             load8(vec + 2 * kC + 32 * s2 + 8 * q, be[s2]);
-            if (vtile) {
-                col_values(st + St::kV, s2, 16 * wave, lane, x);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int64_t t = t0 + 32 * s2 + 8 * q + j;
-                    x[j] = ok && t < len ? Elem<T>::load(v, t * vstride + col) : 0.f;
-                }
-            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                E[s2][j] = x[j] - ga[j] * acc[2 * s2 + (j >> 2)][j & 3];
+                E[s2][j] = v8[s2][j] - ga[j] * acc[2 * s2 + (j >> 2)][j & 3];
                 x[j] = be[s2][j] * E[s2][j];
             }
             split8<3>(x, Y[s2]);
@@ -767,33 +809,25 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_chunk_kernel(Params p) {
             }
         }
         if constexpr (OUT) {
+            // operands exchanged: y^T, whose rows (4 in a lane) are columns v
 #pragma unroll
-            for (int t = 0; t < 4; ++t) acc[t] = zero4();
+            for (int t = 0; t < 4; ++t) out[t] = zero4();
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 Planes<kN> a[4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) a[t] = row_frag<kN, kPitch>(st + St::kQ, t, s, lane);
-                mma_tiles<kO>(a, Sp[s], acc);
+                mma_tiles<kO>(Sp[s], a, out);
             }
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                float ga[8];
-                load8(vec + 32 * s + 8 * q, ga);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[2 * s + (j >> 2)][j & 3] *= ga[j] * p.scale;
-            }
+            for (int t = 0; t < 4; ++t) out[t] *= vec[tile_row(t, lane & 15)] * p.scale;
             Planes<kO> a[4], a2[2];
 #pragma unroll
             for (int t = 0; t < 4; ++t) a[t] = frag<kO>(pf, tri_lower(t, 0), kTri, lane);
 #pragma unroll
             for (int t = 0; t < 2; ++t) a2[t] = frag<kO>(pf, tri_lower(2 + t, 1), kTri, lane);
-            mma_tiles<kO>(a, U[0], acc);
-            mma_tiles<kO>(a2, U[1], acc + 2);
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) out[s][j] = acc[2 * s + (j >> 2)][j & 3];
+            mma_tiles<kO>(U[0], a, out);
+            mma_tiles<kO>(U[1], a2, out + 2);
         }
     }
     if (OUT && chunks > 0) put_out(chunks - 1);

@@ -33,8 +33,8 @@ struct GradParams {
 };
 
 // The mirror of delta_chunk_kernel, backwards over the chunks.
-template <typename T, int KS, int NW, int NBUF>
-__global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp) {
+template <typename T, int KS, int NW, int NBUF, bool VT>
+__global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(GradParams gp) {
     constexpr int kN = PlanesOf<T>::kIn, kPitch = pitch_of<KS>(), kUnits = 2 * kSplit + 1;
     constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;
     using St = Stage<T, KS, kUnits, true>;
@@ -50,7 +50,6 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
     const int64_t vstride = p.Hv * p.V;
     const T* dy = static_cast<const T*>(gp.dy) + (b * p.L * p.Hv + h) * p.V;
     T* dv = static_cast<T*>(gp.dv) + (b * p.L * p.Hv + h) * p.V;
-    const bool vtile = sizeof(T) == 2 && gp.vec_dy;
 
     const KeyCopy<T, KS, NW> keys(p, b, hk, len, wave, lane);
     const int64_t cols = p.V - col0;
@@ -60,7 +59,7 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
         stage_block<kUnits, NW>(st, p.blk + (bh * p.nC + c) * block_units<T, true>() * kFrag, wave, lane);
         keys(st + St::kK, p.kr, c);
         keys(st + St::kQ, p.qr, c);
-        if (vtile) {
+        if constexpr (VT) {
             const int64_t left = len - c * kC;
             values(st + St::kV, reinterpret_cast<const uint16_t*>(dy) + c * kC * vstride + col0,
                    left < 64 ? static_cast<int>(left) : 64);
@@ -104,6 +103,8 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
             split8<3>(x, Sp[s]);
             put_planes<Sl::kO, kPitch>(ws, slab_off, slab_row, Sl::kDs, 4 * s + q, Sp[s]);
         }
+        float dy8[2][8];
+        column_values<T, VT>(dy8, st + St::kV, dy + t0 * vstride, len - t0, ystep, ok ? col : -1, wave, lane);
         Planes<kN> dO[2];
         Planes<3> gO[2], Y[2], gE[2];
         float du[2][8], ga[2][8], be[2][8];
@@ -112,19 +113,10 @@ __global__ void __launch_bounds__(64 * NW, 1) delta_adjoint_kernel(GradParams gp
             float x[8];
             load8(vec + 32 * s + 8 * q, ga[s]);
             load8(vec + 2 * kC + 32 * s + 8 * q, be[s]);
-            if (vtile) {
-                col_values(st + St::kV, s, 16 * wave, lane, x);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int64_t t = t0 + 32 * s + 8 * q + j;
-                    x[j] = ok && t < len ? Elem<T>::load(dy, t * vstride + col) : 0.f;
-                }
-            }
-            split8<kN>(x, dO[s]);
+            split8<kN>(dy8[s], dO[s]);
             put_planes<kN, 64>(ws, slab_off, slab_row, Sl::kDy, 4 * s + q, dO[s]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= ga[s][j] * p.scale;
+            for (int j = 0; j < 8; ++j) x[j] = dy8[s][j] * (ga[s][j] * p.scale);
             split8<3>(x, gO[s]);
         }
         f32x4 acc[4] = {zero4(), zero4(), zero4(), zero4()};
