@@ -97,18 +97,34 @@ struct Planes {
     bf16x8 p[N];
 };
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Two values are rounded by one instruction, and what a rounding leaves is one
+// dot product with (-1, 0) or (0, -1) each, exact as the difference has at most
+// 24 bits: 3.5 instructions a value for three planes.
 template <int N>
 __device__ __forceinline__ void split8(const float (&x)[8], Planes<N>& o) {
-    float r[8];
+    // in registers: as an inline constant, a packed (-1, 0) is not read as one
+    uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
+    asm("" : "+s"(lo), "+s"(hi));
+    const bf16x2 low = __builtin_bit_cast(bf16x2, lo), high = __builtin_bit_cast(bf16x2, hi);
+    u32x4 w[N];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = x[j];
+    for (int j = 0; j < 8; j += 2) {
+        float a = x[j], b = x[j + 1];
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            o.p[n][j] = static_cast<__bf16>(r[j]);
-            if (n + 1 < N) r[j] -= static_cast<float>(o.p[n][j]);
+        for (int n = 0; n < N; ++n) {
+            const bf16x2 h = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+            w[n][j / 2] = __builtin_bit_cast(uint32_t, h);
+            if (n + 1 < N) {
+                a = __builtin_amdgcn_fdot2_f32_bf16(h, low, a, false);
+                b = __builtin_amdgcn_fdot2_f32_bf16(h, high, b, false);
+            }
         }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) o.p[n] = __builtin_bit_cast(bf16x8, w[n]);
 }
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -210,8 +226,6 @@ __device__ __forceinline__ void barrier() {  // every wave's LDS reads are done;
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // `bytes` of memory from `base` (both the same in every lane) as a raw buffer
 __device__ __forceinline__ u32x4 window(const void* base, uint32_t bytes) {
