@@ -250,12 +250,12 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // dst + 16 l of LDS, zeros where `off` is outside.  In assembly because the
 // compiler waits for every copy in flight before any read of LDS; here
 // wait_copies() and barrier() order the two, and the other buffer's copies
-// stay in flight.  No register receives anything.
+// stay in flight.  No register receives anything.  (A volatile statement keeps
+// its place among those two; reads of the buffer in use may pass it.)
 __device__ __forceinline__ void copy16(uint32_t dst, u32x4 from, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(from)
-                 : "memory");
+                 : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(from));
 }
 
 constexpr uint32_t kNowhere = 0x40000000u;  // beyond every window, also with a row's offset added
@@ -288,13 +288,13 @@ struct RowCopy {
     }
 };
 
-// Copies UNITS KiB as they are.
-template <int UNITS, int NW>
-__device__ __forceinline__ void stage_block(uint16_t* dst, const uint16_t* src, int wave, int lane) {
-    const u32x4 w = window(src, UNITS * 1024);
+// Copies units FROM .. UNITS - 1 (KiB) as they are; !some: zeros, and nothing is read.
+template <int FROM, int UNITS, int NW>
+__device__ __forceinline__ void stage_block(uint16_t* dst, const uint16_t* src, bool some, int wave, int lane) {
+    const u32x4 w = window(src, some ? UNITS * 1024 : 0);
     const uint32_t at = lds_offset(dst) + wave * 1024, off = wave * 1024 + lane * 16;
 #pragma unroll
-    for (int i = 0; i < UNITS; i += NW)
+    for (int i = FROM; i < UNITS; i += NW)
         if (i + NW <= UNITS || wave < UNITS - i) copy16(at + i * 1024, w, i * 1024 + off);
 }
 
@@ -356,22 +356,21 @@ struct KeyCopy {
     static constexpr int kPitch = pitch_of<KS>(), kN = PlanesOf<T>::kIn;
     RowCopy<kPitch, NW> copy;
     int64_t head, step, plane;  // the head's first row, and elements from chunk to chunk and plane to plane
-    int64_t len;
     bool packed;
 
-    __device__ __forceinline__ KeyCopy(const Params& p, int64_t b, int64_t hk, int64_t len, int wave, int lane)
+    __device__ __forceinline__ KeyCopy(const Params& p, int64_t b, int64_t hk, int wave, int lane)
         : copy(kN > 1 || p.packed ? kPitch : p.Hk * p.K, kN > 1 || p.packed ? kPitch / 8 : static_cast<int>(p.K / 8),
                wave, lane),
-          len(len), packed(kN > 1 || p.packed) {
+          packed(kN > 1 || p.packed) {
         plane = packed ? 64 * kPitch : 0;
         step = packed ? kN * 64 * kPitch : kC * p.Hk * p.K;
         head = packed ? (b * p.Hk + hk) * p.nC * step : (b * p.L * p.Hk + hk) * p.K;
     }
-    __device__ __forceinline__ void operator()(uint16_t* dst, const uint16_t* x, int64_t c) const {
-        const int64_t left = len - c * kC;
-        const int rows = packed || left >= 64 ? 64 : static_cast<int>(left);
+    // chunk c, `rows` of whose rows are there (none: zeros)
+    __device__ __forceinline__ void operator()(uint16_t* dst, const uint16_t* x, int64_t c, int rows) const {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) copy(dst + i * 64 * kPitch, x + head + c * step + i * plane, rows);
+        for (int i = 0; i < kN; ++i)
+            copy(dst + i * 64 * kPitch, x + head + c * step + i * plane, packed && rows > 0 ? 64 : rows);
     }
 };
 
@@ -444,9 +443,10 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
     const int64_t len = row_len(p.lengths, b, p.L);
     if (t0 >= len) return;
     uint16_t* blk = p.blk + static_cast<int64_t>(blockIdx.x) * block_units<T, BWD>() * kFrag;
-    const KeyCopy<T, KS, 4> keys(p, b, hk, len, wave, lane);
-    keys(s_k, p.kr, c);
-    keys(s_q, p.qr, c);
+    const KeyCopy<T, KS, 4> keys(p, b, hk, wave, lane);
+    const int rows = len - t0 < 64 ? static_cast<int>(len - t0) : 64;
+    keys(s_k, p.kr, c, rows);
+    keys(s_q, p.qr, c, rows);
     if (wave == 0) {
         const bool ok = t0 + lane < len;
         const int64_t i = (b * p.L + t0 + lane) * p.Hv + h;
@@ -688,20 +688,30 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
     static_assert(!VT || sizeof(T) == 2, "a tile of values is one bf16 plane");
     const uint32_t ystep = static_cast<uint32_t>(vstride * sizeof(T));
 
-    const KeyCopy<T, KS, NW> keys(p, b, hk, len, wave, lane);
+    const KeyCopy<T, KS, NW> keys(p, b, hk, wave, lane);
     const int64_t cols = p.V - col0;
     const RowCopy<64, NW> values(vstride, static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
-    const auto issue = [&](int64_t c) {
+    // a chunk's copies in five parts, placed between the products: all at once
+    // they would hold up the wave until the copies before them are under way
+    // (18 a wave: 2,000 of 9,700 cycles a chunk)
+    constexpr int kHalf = (kUnits / 2 + NW - 1) / NW * NW;
+    const auto issue = [&](int64_t c, int part) {  // behind the last chunk: empty windows
         uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
-        const uint16_t* blk = p.blk + (bh * p.nC + c) * block_units<T, !OUT>() * kFrag;
-        stage_block<kUnits, NW>(st, blk + Blk::kVec * kFrag, wave, lane);
-        keys(st + St::kK, p.kr, c);
-        if constexpr (OUT) keys(st + St::kQ, p.qr, c);
-        if constexpr (VT) {
-            const int64_t left = len - c * kC;
-            values(st + St::kV, reinterpret_cast<const uint16_t*>(v) + c * kC * vstride + col0,
-                   left < 64 ? static_cast<int>(left) : 64);
-        }
+        const uint16_t* blk = p.blk + ((bh * p.nC + c) * block_units<T, !OUT>() + Blk::kVec) * kFrag;
+        const int64_t left = len - c * kC;
+        const int rows = left > 64 ? 64 : left > 0 ? static_cast<int>(left) : 0;
+        if (part == 0) keys(st + St::kK, p.kr, c, rows);
+        if (part == 1) stage_block<0, kHalf, NW>(st, blk, rows > 0, wave, lane);
+        if (part == 2) stage_block<kHalf, kUnits, NW>(st, blk, rows > 0, wave, lane);
+        if constexpr (VT)
+            if (part == 3)
+                values(st + St::kV, reinterpret_cast<const uint16_t*>(v) + c * kC * vstride + col0, rows);
+        if constexpr (OUT)
+            if (part == 4) keys(st + St::kQ, p.qr, c, rows);
+    };
+    const auto issue_all = [&](int64_t c) {
+#pragma unroll
+        for (int part = 0; part < 5; ++part) issue(c, part);
     };
 
     f32x4 S[2 * KS];
@@ -729,15 +739,14 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
     const uint32_t slab_off = col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
     const uint32_t slab_bytes = static_cast<uint32_t>(VP / 32) * (Sl::kElements * 2);
     const int slab_row = static_cast<int>(col % 32);
-    if (NBUF == 2 && chunks > 0) issue(0);
+    if (NBUF == 2 && chunks > 0) issue_all(0);
     for (int64_t c = 0; c < chunks; ++c) {
         if constexpr (NBUF == 2) {
             wait_copies();
             barrier();
-            if (c + 1 < chunks) issue(c + 1);
         } else {
             barrier();
-            issue(c);
+            issue_all(c);
             wait_copies();
             barrier();
         }
@@ -748,6 +757,7 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
         column_values<T, VT>(v8, st + St::kV, v + c * kC * vstride, len - c * kC, ystep, ok ? col : -1, wave, lane);
         const uint16_t *xf = st + kFrag, *pf = st + (1 + kSplit) * kFrag;
         const int64_t bhc = bh * p.nC + c;
+        if constexpr (NBUF == 2) issue(c + 1, 0);
         const rsrc_t ws = buffer(OUT ? nullptr : p.slab + bhc * (slab_bytes / 2), slab_bytes);
         Planes<3> Sp[KS];
 #pragma unroll
@@ -758,6 +768,10 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
             split8<3>(x, Sp[s]);
             if constexpr (!OUT) put_planes<kO, kPitch>(ws, slab_off, slab_row, Sl::kS, 4 * s + q, Sp[s]);
         }
+        if constexpr (NBUF == 2) {
+            issue(c + 1, 3);
+            issue(c + 1, 4);
+        }
         // E^ and U; this lane's steps are 32 s + 8 q + 0 .. 7
         f32x4 acc[4] = {zero4(), zero4(), zero4(), zero4()};
 #pragma unroll
@@ -767,6 +781,7 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
             for (int t = 0; t < 4; ++t) a[t] = row_frag<kN, kPitch>(st + St::kK, t, s, lane);
             mma_tiles<3>(a, Sp[s], acc);
         }
+        if constexpr (NBUF == 2) issue(c + 1, 1);
         float E[2][8], be[2][8];
         Planes<3> Y[2];
 #pragma unroll
@@ -792,6 +807,7 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
             mma_tiles<3>(a, Y[0], acc);
             mma_tiles<3>(a2, Y[1], acc + 2);
         }
+        if constexpr (NBUF == 2) issue(c + 1, 2);
         Planes<kO> U[2];
         Planes<3> W[2];
 #pragma unroll
@@ -844,6 +860,7 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
             mma_tiles<kO>(U[1], a2, out + 2);
         }
     }
+    wait_copies();  // none may land once the workgroup's LDS is another's
     if (OUT && chunks > 0) put_out(chunks - 1);
     if (OUT && p.h_last) store_state<KS>(p.h_last + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
 }

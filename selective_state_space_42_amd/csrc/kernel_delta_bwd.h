@@ -51,19 +51,28 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
     const T* dy = static_cast<const T*>(gp.dy) + (b * p.L * p.Hv + h) * p.V;
     T* dv = static_cast<T*>(gp.dv) + (b * p.L * p.Hv + h) * p.V;
 
-    const KeyCopy<T, KS, NW> keys(p, b, hk, len, wave, lane);
+    const KeyCopy<T, KS, NW> keys(p, b, hk, wave, lane);
     const int64_t cols = p.V - col0;
     const RowCopy<64, NW> values(vstride, static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
-    const auto issue = [&](int64_t c) {
+    // in six parts between the products, as in delta_chunk_kernel
+    constexpr int kThird = (kUnits / 3 + NW - 1) / NW * NW;
+    const auto issue = [&](int64_t c, int part) {  // before the first chunk: empty windows
         uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
-        stage_block<kUnits, NW>(st, p.blk + (bh * p.nC + c) * block_units<T, true>() * kFrag, wave, lane);
-        keys(st + St::kK, p.kr, c);
-        keys(st + St::kQ, p.qr, c);
-        if constexpr (VT) {
-            const int64_t left = len - c * kC;
-            values(st + St::kV, reinterpret_cast<const uint16_t*>(dy) + c * kC * vstride + col0,
-                   left < 64 ? static_cast<int>(left) : 64);
-        }
+        const uint16_t* blk = p.blk + (bh * p.nC + c) * block_units<T, true>() * kFrag;
+        const int64_t left = len - c * kC;
+        const int rows = c < 0 ? 0 : left > 64 ? 64 : static_cast<int>(left);
+        if (part == 0) keys(st + St::kK, p.kr, c, rows);
+        if (part == 1) stage_block<0, kThird, NW>(st, blk, rows > 0, wave, lane);
+        if (part == 2) stage_block<kThird, 2 * kThird, NW>(st, blk, rows > 0, wave, lane);
+        if (part == 3) stage_block<2 * kThird, kUnits, NW>(st, blk, rows > 0, wave, lane);
+        if constexpr (VT)
+            if (part == 4)
+                values(st + St::kV, reinterpret_cast<const uint16_t*>(dy) + c * kC * vstride + col0, rows);
+        if (part == 5) keys(st + St::kQ, p.qr, c, rows);
+    };
+    const auto issue_all = [&](int64_t c) {
+#pragma unroll
+        for (int part = 0; part < 6; ++part) issue(c, part);
     };
     using Sl = Slab<T, KS>;
     const uint32_t slab_off = col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
@@ -76,15 +85,14 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
     load_state<KS>(gp.dh_last ? gp.dh_last + (bh * p.V + (ok ? col : 0)) * p.K : nullptr, p.K, ok, lane, S);
     for (int64_t t = chunks * kC + q; t < p.L; t += 4)
         if (ok) Elem<T>::store(dv, t * vstride + col, 0.f);
-    if (NBUF == 2 && chunks > 0) issue(chunks - 1);
+    if (NBUF == 2 && chunks > 0) issue_all(chunks - 1);
     for (int64_t c = chunks - 1; c >= 0; --c) {
         if constexpr (NBUF == 2) {
             wait_copies();
             barrier();
-            if (c > 0) issue(c - 1);
         } else {
             barrier();
-            issue(c);
+            issue_all(c);
             wait_copies();
             barrier();
         }
@@ -92,6 +100,7 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
         const float* vec = reinterpret_cast<const float*>(st + Blk::kVec * kFrag);
         const uint16_t *xtf = st + Blk::kXt * kFrag, *ptf = st + Blk::kPt * kFrag;
         const int64_t t0 = c * kC, bhc = bh * p.nC + c;
+        if constexpr (NBUF == 2) issue(c - 1, 0);
         const rsrc_t ws = buffer(p.slab + bhc * (slab_bytes / 2), slab_bytes);
         const rsrc_t wv = buffer(dv + t0 * vstride, static_cast<uint32_t>(p.L - t0 < 64 ? p.L - t0 : 64) * ystep);
         Planes<3> Sp[KS];
@@ -105,6 +114,10 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
         }
         float dy8[2][8];
         column_values<T, VT>(dy8, st + St::kV, dy + t0 * vstride, len - t0, ystep, ok ? col : -1, wave, lane);
+        if constexpr (NBUF == 2) {
+            issue(c - 1, 4);
+            issue(c - 1, 5);
+        }
         Planes<kN> dO[2];
         Planes<3> gO[2], Y[2], gE[2];
         float du[2][8], ga[2][8], be[2][8];
@@ -119,6 +132,7 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
             for (int j = 0; j < 8; ++j) x[j] = dy8[s][j] * (ga[s][j] * p.scale);
             split8<3>(x, gO[s]);
         }
+        if constexpr (NBUF == 2) issue(c - 1, 1);
         f32x4 acc[4] = {zero4(), zero4(), zero4(), zero4()};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -134,6 +148,7 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[2 * s + (j >> 2)][j & 3] *= w[j];
         }
+        if constexpr (NBUF == 2) issue(c - 1, 2);
         // upper triangles: steps 32 .. 63 reach all four row tiles, 0 .. 31 the first two
         const auto upper = [&](const uint16_t* f, const auto& first, const auto& second) {
             Planes<3> a[4], a2[2];
@@ -155,6 +170,7 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
             }
             split8<3>(x, Y[s]);
         }
+        if constexpr (NBUF == 2) issue(c - 1, 3);
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t] = zero4();
         upper(xtf, Y[0], Y[1]);
@@ -191,6 +207,7 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
             }
         }
     }
+    wait_copies();  // none may land once the workgroup's LDS is another's
     if (gp.dh0) store_state<KS>(gp.dh0 + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
 }
 
@@ -245,8 +262,9 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
     f32x4 dq_all[2 * KS], dk_all[2 * KS];
 #pragma unroll
     for (int t = 0; t < 2 * KS; ++t) dq_all[t] = dk_all[t] = zero4();
-    const KeyCopy<T, KS, 4> keys(p, b, hk, len, wave, lane);
+    const KeyCopy<T, KS, 4> keys(p, b, hk, wave, lane);
     const int slabs = static_cast<int>(p.VP / 32);
+    const int rows = len - t0 < 64 ? static_cast<int>(len - t0) : 64;
     for (int64_t hv = hk * group; hv < (hk + 1) * group; ++hv) {
         const int64_t gate = (b * p.L + t0 + lane) * p.Hv + hv;
         if (t0 >= len) {
@@ -279,7 +297,8 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
         float bound = 0.f;
         for (int sl = 0; sl < slabs; ++sl) {
             barrier();
-            stage_block<Sl::kElements / kFrag, 4>(s_buf, p.slab + (bhc * slabs + sl) * Sl::kElements, wave, lane);
+            stage_block<0, Sl::kElements / kFrag, 4>(s_buf, p.slab + (bhc * slabs + sl) * Sl::kElements, true, wave,
+                                                     lane);
             wait_copies();
             barrier();
             const uint16_t *sE = s_buf + Sl::kE, *sR = s_buf + Sl::kDr, *sY = s_buf + Sl::kDy;
@@ -326,8 +345,8 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
             }
         }
         barrier();
-        keys(s_k, p.kr, c);
-        keys(s_q, p.qr, c);
+        keys(s_k, p.kr, c, rows);
+        keys(s_q, p.qr, c, rows);
         // decays and masks, then the blocks as right operands: k step s = tiles 2s, 2s + 1.
         // dbeta is the diagonal of dR E^^T.
         Planes<kO> a1[2], a2[2], b1[2], b2[2];
