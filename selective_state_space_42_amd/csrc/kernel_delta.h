@@ -85,6 +85,14 @@ __device__ __forceinline__ int tile_row(int t, int m) { return 32 * (t >> 1) + 8
 __device__ __forceinline__ int tri_lower(int t, int s) { return t < 2 ? t : 2 * t - 2 + s; }
 __device__ __forceinline__ int tri_upper(int t, int s) { return t < 2 ? 2 * t + s : t + 2; }
 
+// Workgroups go to the 8 XCDs in turn, each with an L2 of its own: the block
+// that stands for `block` of `n` gives every XCD a run of neighbours, so that the
+// workgroups that share keys and fragments share an L2.
+__device__ __forceinline__ int64_t xcd_run(int64_t block, int64_t n) {
+    const int64_t x = block % 8, per = n / 8, more = n % 8;
+    return x * per + (x < more ? x : more) + block / 8;
+}
+
 __device__ __forceinline__ int row_len(const int32_t* lengths, int64_t b, int64_t L) {
     if (!lengths) return static_cast<int>(L);
     const int64_t n = lengths[b];
@@ -366,11 +374,10 @@ struct KeyCopy {
         step = packed ? kN * 64 * kPitch : kC * p.Hk * p.K;
         head = packed ? (b * p.Hk + hk) * p.nC * step : (b * p.L * p.Hk + hk) * p.K;
     }
-    // chunk c, `rows` of whose rows are there (none: zeros)
-    __device__ __forceinline__ void operator()(uint16_t* dst, const uint16_t* x, int64_t c, int rows) const {
+    // the chunk whose first row is at `x`, `rows` of whose rows are there (none: zeros)
+    __device__ __forceinline__ void operator()(uint16_t* dst, const uint16_t* x, int rows) const {
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-            copy(dst + i * 64 * kPitch, x + head + c * step + i * plane, packed && rows > 0 ? 64 : rows);
+        for (int i = 0; i < kN; ++i) copy(dst + i * 64 * kPitch, x + i * plane, packed && rows > 0 ? 64 : rows);
     }
 };
 
@@ -445,8 +452,8 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
     uint16_t* blk = p.blk + static_cast<int64_t>(blockIdx.x) * block_units<T, BWD>() * kFrag;
     const KeyCopy<T, KS, 4> keys(p, b, hk, wave, lane);
     const int rows = len - t0 < 64 ? static_cast<int>(len - t0) : 64;
-    keys(s_k, p.kr, c, rows);
-    keys(s_q, p.qr, c, rows);
+    keys(s_k, p.kr + keys.head + c * keys.step, rows);
+    keys(s_q, p.qr + keys.head + c * keys.step, rows);
     if (wave == 0) {
         const bool ok = t0 + lane < len;
         const int64_t i = (b * p.L + t0 + lane) * p.Hv + h;
@@ -677,7 +684,8 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
     using Blk = Block<!OUT>;
     extern __shared__ __align__(16) uint16_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
-    const int64_t VP = p.VP, vt = blockIdx.x % p.nV, bh = blockIdx.x / p.nV, b = bh / p.Hv, h = bh % p.Hv;
+    const int64_t block = xcd_run(blockIdx.x, gridDim.x), vt = block % p.nV, bh = block / p.nV;
+    const int64_t VP = p.VP, b = bh / p.Hv, h = bh % p.Hv;
     const int64_t hk = h / (p.Hv / p.Hk);
     const int64_t col0 = vt * 16 * NW, col = col0 + 16 * wave + (lane & 15);
     const bool ok = col < p.V;
@@ -694,24 +702,35 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
     // a chunk's copies in five parts, placed between the products: all at once
     // they would hold up the wave until the copies before them are under way
     // (18 a wave: 2,000 of 9,700 cycles a chunk)
-    constexpr int kHalf = (kUnits / 2 + NW - 1) / NW * NW;
-    const auto issue = [&](int64_t c, int part) {  // behind the last chunk: empty windows
-        uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
-        const uint16_t* blk = p.blk + ((bh * p.nC + c) * block_units<T, !OUT>() + Blk::kVec) * kFrag;
-        const int64_t left = len - c * kC;
-        const int rows = left > 64 ? 64 : left > 0 ? static_cast<int>(left) : 0;
-        if (part == 0) keys(st + St::kK, p.kr, c, rows);
-        if (part == 1) stage_block<0, kHalf, NW>(st, blk, rows > 0, wave, lane);
-        if (part == 2) stage_block<kHalf, kUnits, NW>(st, blk, rows > 0, wave, lane);
+    constexpr int kHalf = kUnits / 2 / NW * NW;
+    const uint16_t* blk = p.blk + (bh * p.nC * block_units<T, !OUT>() + Blk::kVec) * kFrag;
+    const uint16_t *kr = p.kr + keys.head, *qr = p.qr + keys.head, *vr = reinterpret_cast<const uint16_t*>(v) + col0;
+    // where the next chunk goes, and how many of its rows there are (none behind the last: empty windows)
+    uint16_t* st_next = smem;
+    int rows = len < 64 ? static_cast<int>(len) : 64;
+    const auto issue = [&](int part) __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (part == 0) keys(st_next + St::kK, kr, rows);
+        if (part == 1) stage_block<0, kHalf, NW>(st_next, blk, rows > 0, wave, lane);
+        if (part == 2) stage_block<kHalf, kUnits, NW>(st_next, blk, rows > 0, wave, lane);
         if constexpr (VT)
-            if (part == 3)
-                values(st + St::kV, reinterpret_cast<const uint16_t*>(v) + c * kC * vstride + col0, rows);
+            if (part == 3) values(st_next + St::kV, vr, rows);
         if constexpr (OUT)
-            if (part == 4) keys(st + St::kQ, p.qr, c, rows);
+            if (part == 4) keys(st_next + St::kQ, qr, rows);
+        __builtin_amdgcn_sched_barrier(0);
     };
-    const auto issue_all = [&](int64_t c) {
+    const auto issue_all = [&] {
 #pragma unroll
-        for (int part = 0; part < 5; ++part) issue(c, part);
+        for (int part = 0; part < 5; ++part) issue(part);
+    };
+    const auto advance = [&](int64_t c) {  // to the chunk behind c
+        const int64_t left = len - (c + 1) * kC;
+        rows = left > 64 ? 64 : left > 0 ? static_cast<int>(left) : 0;
+        blk += block_units<T, !OUT>() * kFrag;
+        kr += keys.step;
+        qr += keys.step;
+        vr += kC * vstride;
+        if constexpr (NBUF == 2) st_next = smem + ((c + 1) & 1) * St::kElements;
     };
 
     f32x4 S[2 * KS];
@@ -720,33 +739,36 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
     // step of tile t, columns 4 q + 0 .. 3 of the wave's
     f32x4 out[4];
     const uint32_t ycol = static_cast<uint32_t>(col0 + 16 * wave + 4 * q);
+    const uint32_t yoff = ycol < p.V ? tile_row(0, lane & 15) * ystep + ycol * sizeof(T) : kNowhere;
     const auto put_out = [&](int64_t c) {  // rows behind the length are outside the window
         const int64_t left = len - c * kC;
         const rsrc_t w = buffer(y + c * kC * vstride, static_cast<uint32_t>(left < 64 ? left : 64) * ystep);
+        if (p.vec_y) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const uint32_t off = tile_row(t, lane & 15) * ystep + ycol * sizeof(T);
-            if (p.vec_y) {
-                put4<T>(w, ycol < p.V ? off : kNowhere, out[t]);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    Buf<T>::store(w, ycol + r < p.V ? off + r * sizeof(T) : kNowhere, out[t][r]);
-            }
+            for (int t = 0; t < 4; ++t) put4<T>(w, yoff + tile_row(t, 0) * ystep, out[t]);
+            return;
         }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                Buf<T>::store(w, ycol + r < p.V ? yoff + tile_row(t, 0) * ystep + r * sizeof(T) : kNowhere, out[t][r]);
     };
     using Sl = Slab<T, KS>;
     const uint32_t slab_off = col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
     const uint32_t slab_bytes = static_cast<uint32_t>(VP / 32) * (Sl::kElements * 2);
     const int slab_row = static_cast<int>(col % 32);
-    if (NBUF == 2 && chunks > 0) issue_all(0);
+    if (NBUF == 2 && chunks > 0) issue_all();
     for (int64_t c = 0; c < chunks; ++c) {
         if constexpr (NBUF == 2) {
             wait_copies();
             barrier();
+            advance(c);
+            issue(0);
         } else {
             barrier();
-            issue_all(c);
+            issue_all();
+            advance(c);
             wait_copies();
             barrier();
         }
@@ -757,7 +779,6 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
         column_values<T, VT>(v8, st + St::kV, v + c * kC * vstride, len - c * kC, ystep, ok ? col : -1, wave, lane);
         const uint16_t *xf = st + kFrag, *pf = st + (1 + kSplit) * kFrag;
         const int64_t bhc = bh * p.nC + c;
-        if constexpr (NBUF == 2) issue(c + 1, 0);
         const rsrc_t ws = buffer(OUT ? nullptr : p.slab + bhc * (slab_bytes / 2), slab_bytes);
         Planes<3> Sp[KS];
 #pragma unroll
@@ -769,8 +790,8 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
             if constexpr (!OUT) put_planes<kO, kPitch>(ws, slab_off, slab_row, Sl::kS, 4 * s + q, Sp[s]);
         }
         if constexpr (NBUF == 2) {
-            issue(c + 1, 3);
-            issue(c + 1, 4);
+            issue(3);
+            issue(4);
         }
         // E^ and U; this lane's steps are 32 s + 8 q + 0 .. 7
         f32x4 acc[4] = {zero4(), zero4(), zero4(), zero4()};
@@ -781,7 +802,7 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
             for (int t = 0; t < 4; ++t) a[t] = row_frag<kN, kPitch>(st + St::kK, t, s, lane);
             mma_tiles<3>(a, Sp[s], acc);
         }
-        if constexpr (NBUF == 2) issue(c + 1, 1);
+        if constexpr (NBUF == 2) issue(1);
         float E[2][8], be[2][8];
         Planes<3> Y[2];
 #pragma unroll
@@ -807,7 +828,7 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
             mma_tiles<3>(a, Y[0], acc);
             mma_tiles<3>(a2, Y[1], acc + 2);
         }
-        if constexpr (NBUF == 2) issue(c + 1, 2);
+        if constexpr (NBUF == 2) issue(2);
         Planes<kO> U[2];
         Planes<3> W[2];
 #pragma unroll

@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
     extern __shared__ __align__(16) uint16_t smem[];
     const Params& p = gp.f;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
-    const int64_t VP = p.VP, vt = blockIdx.x % p.nV, bh = blockIdx.x / p.nV, b = bh / p.Hv, h = bh % p.Hv;
+    const int64_t block = xcd_run(blockIdx.x, gridDim.x), vt = block % p.nV, bh = block / p.nV;
+    const int64_t VP = p.VP, b = bh / p.Hv, h = bh % p.Hv;
     const int64_t hk = h / (p.Hv / p.Hk);
     const int64_t col0 = vt * 16 * NW, col = col0 + 16 * wave + (lane & 15);
     const bool ok = col < p.V;
@@ -55,20 +56,22 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
     const int64_t cols = p.V - col0;
     const RowCopy<64, NW> values(vstride, static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
     // in six parts between the products, as in delta_chunk_kernel
-    constexpr int kThird = (kUnits / 3 + NW - 1) / NW * NW;
+    constexpr int kThird = kUnits / 3 / NW * NW;
     const auto issue = [&](int64_t c, int part) {  // before the first chunk: empty windows
+        __builtin_amdgcn_sched_barrier(0);
         uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
         const uint16_t* blk = p.blk + (bh * p.nC + c) * block_units<T, true>() * kFrag;
         const int64_t left = len - c * kC;
         const int rows = c < 0 ? 0 : left > 64 ? 64 : static_cast<int>(left);
-        if (part == 0) keys(st + St::kK, p.kr, c, rows);
+        if (part == 0) keys(st + St::kK, p.kr + keys.head + c * keys.step, rows);
         if (part == 1) stage_block<0, kThird, NW>(st, blk, rows > 0, wave, lane);
         if (part == 2) stage_block<kThird, 2 * kThird, NW>(st, blk, rows > 0, wave, lane);
         if (part == 3) stage_block<2 * kThird, kUnits, NW>(st, blk, rows > 0, wave, lane);
         if constexpr (VT)
             if (part == 4)
                 values(st + St::kV, reinterpret_cast<const uint16_t*>(dy) + c * kC * vstride + col0, rows);
-        if (part == 5) keys(st + St::kQ, p.qr, c, rows);
+        if (part == 5) keys(st + St::kQ, p.qr + keys.head + c * keys.step, rows);
+        __builtin_amdgcn_sched_barrier(0);
     };
     const auto issue_all = [&](int64_t c) {
 #pragma unroll
@@ -345,8 +348,8 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
             }
         }
         barrier();
-        keys(s_k, p.kr, c, rows);
-        keys(s_q, p.qr, c, rows);
+        keys(s_k, p.kr + keys.head + c * keys.step, rows);
+        keys(s_q, p.qr + keys.head + c * keys.step, rows);
         // decays and masks, then the blocks as right operands: k step s = tiles 2s, 2s + 1.
         // dbeta is the diagonal of dR E^^T.
         Planes<kO> a1[2], a2[2], b1[2], b2[2];
