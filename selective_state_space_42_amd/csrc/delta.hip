@@ -27,10 +27,24 @@ int check_desc(const ssm_delta_desc_t* d) {
 }
 
 struct Layout {
-    size_t kr, qr, blk, slab, total;
+    size_t kr, qr, blk, slab, trans, enter, total;
 };
 
 int64_t key_steps(const ssm_delta_desc_t* d) { return (d->dkey + 31) / 32; }
+
+// Segments of the forward that are swept side by side.  The sweep goes through
+// a head's chunks one by one and has a workgroup of 4 waves for 64 columns of
+// a head, so few heads leave most of the 256 CUs idle.  Segments cost a sweep more (each one's
+// transition: V + K columns, without outputs), which pays from about 4 on.
+// (32,768 steps of 20 heads of 128, bf16: 1.86 ms as one segment, 0.87 in 6,
+// 0.92 in 12.)
+int64_t segments(const ssm_delta_desc_t* d) {
+    const int64_t groups = d->batch * d->vheads * ((d->dvalue + 63) / 64), chunks = (d->seqlen + kC - 1) / kC;
+    int64_t n = 256 / groups;
+    if (n > chunks / 8) n = chunks / 8;  // at least 8 chunks each
+    if (n > 16) n = 16;
+    return n >= 4 ? n : 1;
+}
 
 // keys and queries that are copied as they are: bf16 rows of whole 16-byte pieces
 bool plain_rows(const ssm_delta_desc_t* d, const void* q, const void* k) {
@@ -52,7 +66,12 @@ Layout layout(const ssm_delta_desc_t* d, bool bwd) {
     take(o.qr, rows);
     const size_t units = bwd ? block_units<float, true>() : f32 ? block_units<float, false>() : block_units<uint16_t, false>();
     take(o.blk, vc * units * kFrag * 2);
-    if (!bwd) return o;
+    if (!bwd) {
+        const size_t more = static_cast<size_t>(d->batch * d->vheads * (segments(d) - 1)) * d->dkey * 4;
+        take(o.trans, more * ((d->dvalue + 63) / 64 * 64 + (d->dkey + 63) / 64 * 64));
+        take(o.enter, more * d->dvalue);
+        return o;
+    }
     const size_t pitch = KP <= 64 ? 64 : 128, planes = f32 ? 3 : 2;
     take(o.slab, vc * (VP / 32) * (planes * 32 * (2 * pitch + 2 * 64) + (f32 ? 3 : 1) * 32 * 64) * 2);
     return o;
@@ -72,24 +91,33 @@ Params params(const ssm_delta_desc_t* d, const Layout& o, bool bwd, void* worksp
     p.nC = (d->seqlen + kC - 1) / kC;
     p.VP = (d->dvalue + 31) / 32 * 32;
     p.scale = d->scale;
+    p.segs = bwd ? 1 : segments(d);
+    p.seg_chunks = (p.nC + p.segs - 1) / p.segs;
+    p.vt_cols = (d->dvalue + 63) / 64 * 64;
+    p.kt_cols = (d->dkey + 63) / 64 * 64;
+    if (p.segs > 1) {
+        p.trans = reinterpret_cast<float*>(w + o.trans);
+        p.enter = reinterpret_cast<float*>(w + o.enter);
+    }
     return p;
 }
 
 dim3 grid(int64_t n) { return dim3(static_cast<unsigned>(n)); }
 
-template <typename T, int KS, bool OUT, int NW, int NBUF>
+template <typename T, int KS, int MODE, int NW, int NBUF>
 void sweep(Params p, hipStream_t s) {
-    constexpr int units = OUT ? block_units<T, false>() : 1 + kSplit;
-    constexpr int lds = NBUF * Stage<T, KS, units, OUT>::kElements * 2;
+    constexpr int units = MODE == kForward ? block_units<T, false>() : 1 + kSplit;
+    constexpr int lds = NBUF * Stage<T, KS, units, MODE == kForward>::kElements * 2;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
-    p.nV = ((OUT ? p.V : p.VP) + 16 * NW - 1) / (16 * NW);
-    const dim3 g = grid(p.B * p.Hv * p.nV), block(64 * NW);
+    const int64_t cols = MODE == kForward ? p.V : MODE == kStates ? p.VP : p.vt_cols + p.kt_cols;
+    p.nV = (cols + 16 * NW - 1) / (16 * NW);
+    const dim3 g = grid(p.B * p.Hv * (MODE == kTransition ? p.segs - 1 : p.segs) * p.nV), block(64 * NW);
     if constexpr (sizeof(T) == 2)
         if (p.vec_v) {
-            hipLaunchKernelGGL((delta_chunk_kernel<T, KS, OUT, NW, NBUF, true>), g, block, lds, s, p);
+            hipLaunchKernelGGL((delta_chunk_kernel<T, KS, MODE, NW, NBUF, true>), g, block, lds, s, p);
             return;
         }
-    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, OUT, NW, NBUF, false>), g, block, lds, s, p);
+    hipLaunchKernelGGL((delta_chunk_kernel<T, KS, MODE, NW, NBUF, false>), g, block, lds, s, p);
 }
 
 template <typename T, int KS, int NW, int NBUF>
@@ -116,7 +144,11 @@ template <typename T, int KS>
 int fwd(const Params& p, hipStream_t s) {
     constexpr int nbuf = sizeof(T) == 4 ? 1 : 2;
     prepare<T, KS, false>(p, s);
-    sweep<T, KS, true, 4, nbuf>(p, s);
+    if (p.segs > 1) {
+        sweep<T, KS, kTransition, 4, 1>(p, s);
+        hipLaunchKernelGGL(delta_join_kernel, grid(p.B * p.Hv * ((p.V + 7) / 8)), dim3(256), 0, s, p);
+    }
+    sweep<T, KS, kForward, 4, nbuf>(p, s);
     return ssm::launch_status();
 }
 
@@ -124,7 +156,7 @@ template <typename T, int KS>
 int bwd(const GradParams& g, hipStream_t s) {
     constexpr int nbuf = sizeof(T) == 4 ? 1 : 2;
     prepare<T, KS, true>(g.f, s);
-    sweep<T, KS, false, 4, nbuf>(g.f, s);
+    sweep<T, KS, kStates, 4, nbuf>(g.f, s);
     adjoint<T, KS, 4, nbuf>(g, s);
     const dim3 chunks = grid(g.f.B * g.f.Hk * g.f.nC);
     if (g.f.Hv > g.f.Hk)

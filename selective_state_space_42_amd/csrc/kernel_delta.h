@@ -64,6 +64,9 @@ struct Params {
     uint16_t* slab;                 // backward: what delta_grad_kernel reads of the sweeps, see Slab
     int64_t B, L, Hk, Hv, K, V, nC;
     int64_t nV, VP;                 // column groups of a workgroup, and the state's columns in all
+    int64_t segs, seg_chunks;       // segments that are swept side by side, and their chunks
+    float *trans, *enter;           // [B][Hv][segs - 1][VT + KT][K] and [B][Hv][segs - 1][V][K], see delta_join_kernel
+    int64_t vt_cols, kt_cols;       // VT and KT: V and K in whole workgroups' columns
     float scale;
     int32_t packed, vec_v, vec_y;   // kr, qr are packed; rows of v move in 16-byte pieces, those of y in 4 elements
 };
@@ -669,27 +672,37 @@ struct Stage {
     static constexpr int kElements = kV + (sizeof(T) == 2 ? 64 * 64 : 0);
 };
 
+enum Sweep : int { kForward = 0, kStates = 1, kTransition = 2 };
+
 // The recurrence over chunks: one wave per 16 columns of a head's state, NW
 // waves (neighbouring columns) sharing what is staged in LDS.  With two
 // buffers the next chunk's copies run under this chunk's products.
-// OUT: writes y and h_last (the forward); else the states entering each chunk
-// and E^ (what the gradients read).  VT: values are staged too (bf16 rows of
+// kForward writes y and h_last, kStates the states entering each chunk and E^
+// (what the gradients read), kTransition nothing but the states at its
+// segment's end.  VT: values are staged too (bf16 rows of
 // whole 16-byte pieces).
-template <typename T, int KS, bool OUT, int NW, int NBUF, bool VT>
+template <typename T, int KS, int MODE, int NW, int NBUF, bool VT>
 __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
+    constexpr bool OUT = MODE == kForward, BWD = MODE == kStates;
     constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
     constexpr int kUnits = OUT ? block_units<T, false>() : 1 + kSplit;
     constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;  // of the state, at a time
     using St = Stage<T, KS, kUnits, OUT>;
-    using Blk = Block<!OUT>;
+    using Blk = Block<BWD>;
     extern __shared__ __align__(16) uint16_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
-    const int64_t block = xcd_run(blockIdx.x, gridDim.x), vt = block % p.nV, bh = block / p.nV;
+    // column groups of a segment, segments of a head, heads
+    const int64_t block = xcd_run(blockIdx.x, gridDim.x), vt = block % p.nV, rest = block / p.nV;
+    const int64_t segs = MODE == kTransition ? p.segs - 1 : p.segs, seg = rest % segs, bh = rest / segs;
     const int64_t VP = p.VP, b = bh / p.Hv, h = bh % p.Hv;
     const int64_t hk = h / (p.Hv / p.Hk);
     const int64_t col0 = vt * 16 * NW, col = col0 + 16 * wave + (lane & 15);
-    const bool ok = col < p.V;
-    const int64_t len = row_len(p.lengths, b, p.L), chunks = (len + kC - 1) / kC;
+    // behind the values' columns, a transition's: a unit state, and values of 0
+    const bool unit = MODE == kTransition && col0 >= p.vt_cols;
+    const bool ok = !unit && col < p.V;
+    const int64_t len = row_len(p.lengths, b, p.L), all = (len + kC - 1) / kC;
+    const int64_t c0 = seg * p.seg_chunks < all ? seg * p.seg_chunks : all;
+    const int64_t chunks = c0 + p.seg_chunks < all ? c0 + p.seg_chunks : all;  // those from c0 on
     const T* v = static_cast<const T*>(p.v) + (b * p.L * p.Hv + h) * p.V;
     T* y = static_cast<T*>(p.y) + (b * p.L * p.Hv + h) * p.V;
     const int64_t vstride = p.Hv * p.V;
@@ -698,16 +711,18 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
 
     const KeyCopy<T, KS, NW> keys(p, b, hk, wave, lane);
     const int64_t cols = p.V - col0;
-    const RowCopy<64, NW> values(vstride, static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
+    const RowCopy<64, NW> values(vstride, unit ? 0 : static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
     // a chunk's copies in five parts, placed between the products: all at once
     // they would hold up the wave until the copies before them are under way
     // (18 a wave: 2,000 of 9,700 cycles a chunk)
     constexpr int kHalf = kUnits / 2 / NW * NW;
-    const uint16_t* blk = p.blk + (bh * p.nC * block_units<T, !OUT>() + Blk::kVec) * kFrag;
-    const uint16_t *kr = p.kr + keys.head, *qr = p.qr + keys.head, *vr = reinterpret_cast<const uint16_t*>(v) + col0;
+    const uint16_t* blk = p.blk + ((bh * p.nC + c0) * block_units<T, BWD>() + Blk::kVec) * kFrag;
+    const int64_t head = keys.head + c0 * keys.step;
+    const uint16_t *kr = p.kr + head, *qr = p.qr + head;
+    const uint16_t* vr = reinterpret_cast<const uint16_t*>(v) + c0 * kC * vstride + col0;
     // where the next chunk goes, and how many of its rows there are (none behind the last: empty windows)
     uint16_t* st_next = smem;
-    int rows = len < 64 ? static_cast<int>(len) : 64;
+    int rows = len - c0 * kC < 64 ? static_cast<int>(len - c0 * kC) : 64;
     const auto issue = [&](int part) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
         if (part == 0) keys(st_next + St::kK, kr, rows);
@@ -726,15 +741,26 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
     const auto advance = [&](int64_t c) {  // to the chunk behind c
         const int64_t left = len - (c + 1) * kC;
         rows = left > 64 ? 64 : left > 0 ? static_cast<int>(left) : 0;
-        blk += block_units<T, !OUT>() * kFrag;
+        blk += block_units<T, BWD>() * kFrag;
         kr += keys.step;
         qr += keys.step;
         vr += kC * vstride;
-        if constexpr (NBUF == 2) st_next = smem + ((c + 1) & 1) * St::kElements;
+        if constexpr (NBUF == 2) st_next = smem + ((c + 1 - c0) & 1) * St::kElements;
     };
 
     f32x4 S[2 * KS];
-    load_state<KS>(p.h0 ? p.h0 + (bh * p.V + (ok ? col : 0)) * p.K : nullptr, p.K, ok, lane, S);
+    {
+        const int64_t row = ok ? col : 0;
+        const float* h = seg == 0 ? (p.h0 ? p.h0 + (bh * p.V + row) * p.K : nullptr)
+                         : OUT ? p.enter + ((bh * (p.segs - 1) + seg - 1) * p.V + row) * p.K : nullptr;
+        load_state<KS>(h, p.K, ok, lane, S);
+        if (unit)
+#pragma unroll
+            for (int t = 0; t < 2 * KS; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[t][r] = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r == col - p.vt_cols ? 1.f : 0.f;
+    }
     // y^T of the chunk before, stored under this chunk's products: this lane's
     // step of tile t, columns 4 q + 0 .. 3 of the wave's
     f32x4 out[4];
@@ -755,11 +781,11 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
                 Buf<T>::store(w, ycol + r < p.V ? yoff + tile_row(t, 0) * ystep + r * sizeof(T) : kNowhere, out[t][r]);
     };
     using Sl = Slab<T, KS>;
-    const uint32_t slab_off = col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
+    const uint32_t slab_off = BWD && col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
     const uint32_t slab_bytes = static_cast<uint32_t>(VP / 32) * (Sl::kElements * 2);
     const int slab_row = static_cast<int>(col % 32);
-    if (NBUF == 2 && chunks > 0) issue_all();
-    for (int64_t c = 0; c < chunks; ++c) {
+    if (NBUF == 2 && chunks > c0) issue_all();
+    for (int64_t c = c0; c < chunks; ++c) {
         if constexpr (NBUF == 2) {
             wait_copies();
             barrier();
@@ -772,14 +798,14 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
             wait_copies();
             barrier();
         }
-        if (OUT && c > 0) put_out(c - 1);
-        const uint16_t* st = smem + (NBUF == 2 ? (c & 1) * St::kElements : 0);
+        if (OUT && c > c0) put_out(c - 1);
+        const uint16_t* st = smem + (NBUF == 2 ? ((c - c0) & 1) * St::kElements : 0);
         const float* vec = reinterpret_cast<const float*>(st);
         float v8[2][8];
         column_values<T, VT>(v8, st + St::kV, v + c * kC * vstride, len - c * kC, ystep, ok ? col : -1, wave, lane);
         const uint16_t *xf = st + kFrag, *pf = st + (1 + kSplit) * kFrag;
         const int64_t bhc = bh * p.nC + c;
-        const rsrc_t ws = buffer(OUT ? nullptr : p.slab + bhc * (slab_bytes / 2), slab_bytes);
+        const rsrc_t ws = buffer(!BWD ? nullptr : p.slab + bhc * (slab_bytes / 2), slab_bytes);
         Planes<3> Sp[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -787,7 +813,7 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = S[2 * s + (j >> 2)][j & 3];
             split8<3>(x, Sp[s]);
-            if constexpr (!OUT) put_planes<kO, kPitch>(ws, slab_off, slab_row, Sl::kS, 4 * s + q, Sp[s]);
+            if constexpr (BWD) put_planes<kO, kPitch>(ws, slab_off, slab_row, Sl::kS, 4 * s + q, Sp[s]);
         }
         if constexpr (NBUF == 2) {
             issue(3);
@@ -841,8 +867,8 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
                 x[j] = OUT ? u : e;
                 w[j] *= u;
             }
-            split8<kO>(x, U[s2]);  // E^ without beta where it is kept for the gradients
-            if constexpr (!OUT) put_planes<kO, 64>(ws, slab_off, slab_row, Sl::kE, 4 * s2 + q, U[s2]);
+            if constexpr (MODE != kTransition) split8<kO>(x, U[s2]);  // E^ without beta where it is kept for the gradients
+            if constexpr (BWD) put_planes<kO, 64>(ws, slab_off, slab_row, Sl::kE, 4 * s2 + q, U[s2]);
             split8<3>(w, W[s2]);
         }
         // the state first: the next chunk waits for it
@@ -882,8 +908,55 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
         }
     }
     wait_copies();  // none may land once the workgroup's LDS is another's
-    if (OUT && chunks > 0) put_out(chunks - 1);
-    if (OUT && p.h_last) store_state<KS>(p.h_last + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
+    if (OUT && chunks > c0) put_out(chunks - 1);
+    if (MODE == kTransition) {
+        const int64_t n = p.vt_cols + p.kt_cols;
+        store_state<KS>(p.trans + ((bh * segs + seg) * n + col) * p.K, p.K, true, lane, S);
+    }
+    if (OUT && p.h_last && seg == segs - 1) store_state<KS>(p.h_last + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
+}
+
+// The states entering segments 1, 2, ...: with N the state a segment leaves when
+// it starts from 0 (segment 0: from h0) and row e of M the one it leaves when it
+// starts from unit row e without values (both rows of `trans`),
+//   enter_1 = N_0,  enter_{j + 1} = N_j + enter_j M_j.
+// A workgroup takes 8 rows v of a head; thread k % 128 one key element.
+__global__ void __launch_bounds__(256) delta_join_kernel(Params p) {
+    __shared__ __align__(16) float s_s[8][128];
+    const int tid = threadIdx.x, k = tid & 127, half = tid >> 7;  // half: rows 4 half .. 4 half + 3
+    const int64_t vb = blockIdx.x % ((p.V + 7) / 8), bh = blockIdx.x / ((p.V + 7) / 8), n = p.vt_cols + p.kt_cols;
+    float x[4];
+    for (int64_t j = 0; j < p.segs - 1; ++j) {
+        const float* N = p.trans + (bh * (p.segs - 1) + j) * n * p.K;
+        const float* M = N + p.vt_cols * p.K;
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // (the values' columns are there up to a multiple of 8)
+            y[i] = k < p.K ? N[(vb * 8 + 4 * half + i) * p.K + k] : 0.f;
+        if (j > 0) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s_s[4 * half + i][k] = x[i];
+            __syncthreads();
+            // 32 rows of M in flight
+            for (int e0 = 0; e0 < p.K; e0 += 32) {
+                float m[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) m[e] = M[(e0 + e < p.K ? e0 + e : 0) * p.K + (k < p.K ? k : 0)];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e0 + e < p.K)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[i] += s_s[4 * half + i][e0 + e] * m[e];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = y[i];
+            const int64_t v = vb * 8 + 4 * half + i;
+            if (k < p.K && v < p.V) p.enter[((bh * (p.segs - 1) + j) * p.V + v) * p.K + k] = x[i];
+        }
+    }
 }
 
 // ---- the decode step.  Eight lanes share a row v of the state, lane i of them

@@ -106,6 +106,18 @@ def test_strong_decays_keep_their_differences(dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("K,V", [(32, 40), (100, 64)])
+def test_few_heads_and_many_steps(K, V, dtype):
+    """Long enough for segments swept side by side: rows that end in the first
+    segment, inside one, with one, and not at all."""
+    L = 4200
+    lengths = torch.tensor([4200, 30, 0, 2111, 1088], dtype=torch.int32)
+    x = make(5, L, 1, 1, K, V, dtype, seed=18, device="cuda")
+    x["g"] *= 0.05  # states that live on from segment to segment
+    check_fwd(x, dtype, lengths=lengths)
+
+
+@DTYPES
 @pytest.mark.parametrize("cuts", [(70, 130), (64, 1, 63), (5, 123)])
 def test_pieces_and_steps_continue_a_sequence(cuts, dtype):
     """A sequence in pieces, then step by step, as a prompt and its decoding run it."""
