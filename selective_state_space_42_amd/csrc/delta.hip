@@ -258,7 +258,7 @@ int ssm_delta_step(const ssm_delta_desc_t* d, const void* q, const void* k, cons
     p.B = d->batch; p.Hk = d->kheads; p.Hv = d->vheads; p.K = d->dkey; p.V = d->dvalue;
     p.row_blocks = (d->dvalue + 31) / 32;
     p.scale = d->scale;
-    const bool vec = d->dkey % 4 == 0 && ssm::aligned(h, 16);
+    const bool vec = d->dkey % 4 == 0 && ssm::aligned(h, 16) && !misaligned({q, k}, 4 * io_size(d));
     hipStream_t s = static_cast<hipStream_t>(stream);
     return d->io_dtype == SSM_DTYPE_F32 ? step<float>(p, vec, s) : step<uint16_t>(p, vec, s);
 }

@@ -979,6 +979,17 @@ __device__ __forceinline__ float sum8(float x) {
     return x;
 }
 
+// 4 elements at a boundary of their size
+__device__ __forceinline__ void take4(const float* p, float (&x)[4]) {
+    const f32x4 w = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = w[j];
+}
+__device__ __forceinline__ void take4(const uint16_t* p, float (&x)[4]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+}
+
 template <typename T, int NP, bool VEC>
 __global__ void __launch_bounds__(256) delta_step_kernel(StepParams p) {
     const int lane = threadIdx.x & 7;
@@ -992,15 +1003,13 @@ __global__ void __launch_bounds__(256) delta_step_kernel(StepParams p) {
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
         if constexpr (VEC) {
-            const int e = 4 * (lane + 8 * n);
-            const bool in = e < p.K;
-            const f32x4 x = in && ok ? *reinterpret_cast<const f32x4*>(hp + e) : zero4();
+            const int e = 4 * (lane + 8 * n), at = e < p.K ? e : 0;
+            take4(hp + at, s[n]);
+            take4(kp + at, k[n]);
+            take4(qp + at, q[n]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[n][j] = x[j];
-                k[n][j] = in ? Elem<T>::load(kp, e + j) : 0.f;
-                q[n][j] = in ? Elem<T>::load(qp, e + j) : 0.f;
-            }
+            for (int j = 0; j < 4; ++j)  // behind K: nothing predicted, written or read
+                s[n][j] = e < p.K ? s[n][j] : 0.f, k[n][j] = e < p.K ? k[n][j] : 0.f, q[n][j] = e < p.K ? q[n][j] : 0.f;
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

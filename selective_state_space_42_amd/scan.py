@@ -182,25 +182,25 @@ def _check(where: str, io_dtype, specs) -> None:
     """
     if io_dtype not in _IO_DTYPES:
         raise ValueError(f"{where}: I/O dtype must be float32 or bfloat16, got {io_dtype}")
-    device = None
+    first = index = None
     for name, t, shape, dtype in specs:
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{where}: {name} must be a torch.Tensor")
         want = io_dtype if dtype is None else dtype
-        if t.dtype != want:
+        if t.dtype is not want:
             raise ValueError(f"{where}: {name} has dtype {t.dtype}, expected {want}")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous (dense row-major)")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{where}: {name} is on {t.device}, other arguments on {device}")
-    if device is None or device.type != "cuda":
-        raise ValueError(f"{where}: arguments must be GPU tensors (got {device})")
+        if first is None:
+            first, index = t, t.get_device()
+        elif t.get_device() != index or (index < 0 and t.device != first.device):
+            raise ValueError(f"{where}: {name} is on {t.device}, other arguments on {first.device}")
+    if first is None or not first.is_cuda:
+        raise ValueError(f"{where}: arguments must be GPU tensors (got {first.device if first is not None else None})")
 
 
 def _check_workspace(where: str, workspace, device) -> None:
@@ -592,15 +592,27 @@ def ssm_mimo_step(u, delta, A, B, C, D=None, theta=None, lam=None, *, h, u_prev=
     return y
 
 
-def _on(device, stream):
-    """A context in which `device` is the current one and tensors allocated
+_HERE = contextlib.nullcontext()
+
+
+def _on(t, stream):
+    """A context in which t's device is the current one and tensors allocated
     for the call belong to `stream` (a raw hipStream_t, or None), so that the
     allocator does not hand a workspace on while that stream still uses it."""
     if stream is not None:
-        return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
-    if device.index is not None and device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+        return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=t.device))
+    if t.get_device() != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return _HERE
+
+
+# the current stream as a handle, without the Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def make_delta_desc(batch, seqlen, kheads, vheads, dkey, dvalue, io_dtype, scale=None) -> DeltaDesc:
@@ -646,7 +658,7 @@ def ssm_delta_fwd(q, k, v, g, beta, h0=None, *, scale=None, lengths=None, y=None
         ("lengths", lengths, (B,), torch.int32), ("y", y, (B, L, Hv, V), None), ("h_last", h_last, state, f32)])
     _check_workspace(where, workspace, q.device)
     desc = make_delta_desc(B, L, Hk, Hv, K, V, q.dtype, scale)
-    with _on(q.device, stream):
+    with _on(q, stream):
         if y is None:
             y = torch.empty_like(v) if lengths is None else torch.zeros_like(v)
         if h_last is None and want_h_last:
@@ -654,10 +666,10 @@ def ssm_delta_fwd(q, k, v, g, beta, h0=None, *, scale=None, lengths=None, y=None
         if workspace is None:
             workspace = torch.empty(max(ssm_delta_workspace_bytes(desc), 1), dtype=torch.uint8, device=q.device)
         if stream is None:
-            stream = torch.cuda.current_stream(q.device).cuda_stream
-        st = _lib().ssm_delta_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
-                                  _ptr(lengths), _ptr(y), _ptr(h_last), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), ctypes.c_void_p(stream))
+            stream = _raw_stream(q.get_device())
+        st = _lib().ssm_delta_fwd(ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(h0),
+                                  _addr(lengths), _addr(y), _addr(h_last), _addr(workspace),
+                                  workspace.numel() * workspace.element_size(), stream)
     if st != 0:
         raise ScanError(st, where)
     return y, h_last
@@ -679,13 +691,13 @@ def ssm_delta_step(q, k, v, g, beta, *, h, scale=None, y=None, stream=None):
         ("q", q, (B, Hk, K), None), ("k", k, (B, Hk, K), None), ("v", v, (B, Hv, V), None), ("g", g, (B, Hv), None),
         ("beta", beta, (B, Hv), None), ("h", h, (B, Hv, V, K), torch.float32), ("y", y, (B, Hv, V), None)])
     desc = make_delta_desc(B, 1, Hk, Hv, K, V, q.dtype, scale)
-    with _on(q.device, stream):
+    with _on(q, stream):
         if y is None:
             y = torch.empty_like(v)
         if stream is None:
-            stream = torch.cuda.current_stream(q.device).cuda_stream
-        st = _lib().ssm_delta_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h),
-                                   _ptr(y), ctypes.c_void_p(stream))
+            stream = _raw_stream(q.get_device())
+        st = _lib().ssm_delta_step(ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(h),
+                                   _addr(y), stream)
     if st != 0:
         raise ScanError(st, where)
     return y
@@ -707,19 +719,19 @@ def ssm_delta_bwd(q, k, v, g, beta, h0=None, *, dy, dh_last=None, scale=None, le
         ("lengths", lengths, (B,), torch.int32), ("dy", dy, (B, L, Hv, V), None), ("dh_last", dh_last, state, f32)])
     _check_workspace(where, workspace, q.device)
     desc = make_delta_desc(B, L, Hk, Hv, K, V, q.dtype, scale)
-    with _on(q.device, stream):
+    with _on(q, stream):
         out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), dg=torch.empty_like(g),
                    dbeta=torch.empty_like(beta),
                    dh0=torch.empty(state, dtype=f32, device=q.device) if want_dh0 else None)
         if workspace is None:
             workspace = torch.empty(max(ssm_delta_bwd_workspace_bytes(desc), 1), dtype=torch.uint8, device=q.device)
         if stream is None:
-            stream = torch.cuda.current_stream(q.device).cuda_stream
-        st = _lib().ssm_delta_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
-                                  _ptr(lengths), _ptr(dy), _ptr(dh_last),
-                                  *(_ptr(out[n]) for n in ("dq", "dk", "dv", "dg", "dbeta", "dh0")),
-                                  _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                  ctypes.c_void_p(stream))
+            stream = _raw_stream(q.get_device())
+        st = _lib().ssm_delta_bwd(ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(h0),
+                                  _addr(lengths), _addr(dy), _addr(dh_last),
+                                  *(_addr(out[n]) for n in ("dq", "dk", "dv", "dg", "dbeta", "dh0")),
+                                  _addr(workspace), workspace.numel() * workspace.element_size(),
+                                  stream)
     if st != 0:
         raise ScanError(st, where)
     return out
@@ -777,15 +789,15 @@ def _rotary(where, q, k, inv_freq, positions, offset, interleaved, inverse, ampl
         raise ValueError(f"{where}: inv_freq has {half} angles, a head of {K} has {K // 2} pairs")
     desc = RotaryDesc(B, L, Hq, Hk, K, 2 * half, int(offset), float(amplitude), int(bool(interleaved)), int(inverse),
                       SSM_DTYPE[q.dtype])
-    with _on(q.device, stream):
+    with _on(q, stream):
         if q_out is None:
             q_out = torch.empty_like(q)
         if k is not None and k_out is None:
             k_out = torch.empty_like(k)
         if stream is None:
-            stream = torch.cuda.current_stream(q.device).cuda_stream
-        st = _lib().ssm_rotary(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(inv_freq), _ptr(positions), _ptr(q_out),
-                               _ptr(k_out), ctypes.c_void_p(stream))
+            stream = _raw_stream(q.get_device())
+        st = _lib().ssm_rotary(ctypes.byref(desc), _addr(q), _addr(k), _addr(inv_freq), _addr(positions), _addr(q_out),
+                               _addr(k_out), stream)
     if st != 0:
         raise ScanError(st, where)
     return q_out, k_out
