@@ -50,7 +50,6 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
     const int64_t len = row_len(p.lengths, b, p.L), chunks = (len + kC - 1) / kC;
     const int64_t vstride = p.Hv * p.V;
     const T* dy = static_cast<const T*>(gp.dy) + (b * p.L * p.Hv + h) * p.V;
-    T* dv = static_cast<T*>(gp.dv) + (b * p.L * p.Hv + h) * p.V;
 
     const KeyCopy<T, KS, NW> keys(p, b, hk, wave, lane);
     const int64_t cols = p.V - col0;
@@ -82,12 +81,9 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
     const uint32_t slab_bytes = static_cast<uint32_t>(VP / 32) * (Sl::kElements * 2);
     const int slab_row = static_cast<int>(col % 32);
     const uint32_t ystep = static_cast<uint32_t>(vstride * sizeof(T));
-    const uint32_t yoff = ok ? 8 * q * ystep + static_cast<uint32_t>(col * sizeof(T)) : kNowhere;
 
     f32x4 S[2 * KS];
     load_state<KS>(gp.dh_last ? gp.dh_last + (bh * p.V + (ok ? col : 0)) * p.K : nullptr, p.K, ok, lane, S);
-    for (int64_t t = chunks * kC + q; t < p.L; t += 4)
-        if (ok) Elem<T>::store(dv, t * vstride + col, 0.f);
     if (NBUF == 2 && chunks > 0) issue_all(chunks - 1);
     for (int64_t c = chunks - 1; c >= 0; --c) {
         if constexpr (NBUF == 2) {
@@ -105,7 +101,6 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
         const int64_t t0 = c * kC, bhc = bh * p.nC + c;
         if constexpr (NBUF == 2) issue(c - 1, 0);
         const rsrc_t ws = buffer(p.slab + bhc * (slab_bytes / 2), slab_bytes);
-        const rsrc_t wv = buffer(dv + t0 * vstride, static_cast<uint32_t>(p.L - t0 < 64 ? p.L - t0 : 64) * ystep);
         Planes<3> Sp[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -182,10 +177,8 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
             float x[8], dr[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int i = 32 * s2 + 8 * q + j;
                 dr[j] = du[s2][j] - acc[2 * s2 + (j >> 2)][j & 3];
                 const float de = be[s2][j] * dr[j];
-                Buf<T>::store(wv, yoff + (32 * s2 + j) * ystep, t0 + i < len ? de : 0.f);
                 x[j] = -ga[s2][j] * de;
             }
             split8<3>(x, gE[s2]);
@@ -249,7 +242,10 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
     constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
     using Sl = Slab<T, KS>;
     constexpr int kKeys = 2 * kN * 64 * kPitch;
-    __shared__ __align__(16) uint16_t s_buf[kKeys > Sl::kElements ? kKeys : Sl::kElements];
+    // states of a slab and the steps' tiles of two (then keys and queries)
+    constexpr int kStates2 = Sl::kE, kSteps = Sl::kElements - Sl::kE;
+    constexpr int kAll = kStates2 + 2 * kSteps;
+    __shared__ __align__(16) uint16_t s_buf[kKeys > kAll ? kKeys : kAll];
     __shared__ double s_g[kC];
     __shared__ float s_dg[kC], s_db[kC], s_end[4];
     uint16_t *s_k = s_buf, *s_q = s_buf + kN * 64 * kPitch;
@@ -268,6 +264,23 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
     const KeyCopy<T, KS, 4> keys(p, b, hk, wave, lane);
     const int slabs = static_cast<int>(p.VP / 32);
     const int rows = len - t0 < 64 ? static_cast<int>(len - t0) : 64;
+    T* dv = static_cast<T*>(gp.dv);
+    const bool dv_pieces = p.V % 8 == 0 && reinterpret_cast<uintptr_t>(dv) % 16 == 0;
+    // dV of this lane's step, columns v .. v + 7: beta dR
+    const auto put_dv = [&](int64_t hv, int64_t v, const auto& r, float be) __attribute__((always_inline)) {
+        if (tn >= p.L || v >= p.V) return;
+        T* to = dv + ((b * p.L + tn) * p.Hv + hv) * p.V + v;
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = tn < len ? be * plane_sum(r, j) : 0.f;
+        if (dv_pieces) {
+            store8(to, x);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (v + j < p.V) Elem<T>::store(to, j, x[j]);
+    };
     for (int64_t hv = hk * group; hv < (hk + 1) * group; ++hv) {
         const int64_t gate = (b * p.L + t0 + lane) * p.Hv + hv;
         if (t0 >= len) {
@@ -275,6 +288,8 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
                 Elem<T>::store(dg, gate, 0.f);
                 Elem<T>::store(db, gate, 0.f);
             }
+            const Planes<1> none = {};
+            for (int64_t v = 8 * q; v < p.V; v += 32) put_dv(hv, v, none, 0.f);
             continue;
         }
         const int64_t bhc = (b * p.Hv + hv) * p.nC + c;
@@ -298,33 +313,29 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
 #pragma unroll
         for (int t = 0; t < 4; ++t) A1[t] = A2[t] = B1[t] = B2[t] = zero4();
         float bound = 0.f;
+        // a slab's steps are staged while the slab before is used, its states under
+        // the products of its steps
+        const uint16_t* slab = p.slab + bhc * slabs * Sl::kElements;
+        const auto stage_states = [&](int sl) __attribute__((always_inline)) {
+            stage_block<0, kStates2 / kFrag, 4>(s_buf, slab + sl * Sl::kElements, true, wave, lane);
+        };
+        const auto stage_steps = [&](int sl) __attribute__((always_inline)) {
+            stage_block<0, kSteps / kFrag, 4>(s_buf + kStates2 + (sl & 1) * kSteps, slab + sl * Sl::kElements + Sl::kE,
+                                              sl < slabs, wave, lane);
+        };
+        barrier();  // the head before is done with LDS
+        stage_steps(0);
+        stage_states(0);
+        wait_copies();
+        barrier();
         for (int sl = 0; sl < slabs; ++sl) {
-            barrier();
-            stage_block<0, Sl::kElements / kFrag, 4>(s_buf, p.slab + (bhc * slabs + sl) * Sl::kElements, true, wave,
-                                                     lane);
-            wait_copies();
-            barrier();
-            const uint16_t *sE = s_buf + Sl::kE, *sR = s_buf + Sl::kDr, *sY = s_buf + Sl::kDy;
+            const uint16_t *sE = s_buf + kStates2 + (sl & 1) * kSteps, *sR = sE + Sl::kDr - Sl::kE,
+                           *sY = sE + Sl::kDy - Sl::kE;
+            stage_steps(sl + 1);  // (behind the last: nothing is read)
             const Planes<kN> On = col_frag<kN, 64, 32>(sY, wave, 0, lane);
             const Planes<kO> Rn = col_frag<kO, 64, 32>(sR, wave, 0, lane);
             const Planes<kO> En = col_frag<kO, 64, 32>(sE, wave, 0, lane);
-#pragma unroll
-            for (int t = 0; t < 2 * KS; t += 2) {
-                Planes<kO> a[2], d[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    a[i] = col_frag<kO, kPitch, 32>(s_buf + Sl::kS, t + i, 0, lane);
-                    d[i] = col_frag<kO, kPitch, 32>(s_buf + Sl::kDs, t + i, 0, lane);
-                }
-                mma_tiles<kO>(a, On, D1 + t);
-                mma_tiles<kO>(a, Rn, D2 + t);
-                mma_tiles<kO>(d, En, D3 + t);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (((t + i) & 3) == wave)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) bound += plane_sum(a[i], j) * plane_sum(d[i], j);
-            }
+            put_dv(hv, sl * 32 + 8 * q, Rn, be_n);
 #pragma unroll
             for (int t = 0; t < 4; t += 2) {
                 if (t / 2 <= wave / 2) {  // rows j not behind this wave's steps
@@ -346,7 +357,31 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
                     mma_tiles<kO>(r, En, B2 + t);
                 }
             }
+            if (sl > 0) {  // this slab's states
+                wait_copies();
+                barrier();
+            }
+#pragma unroll
+            for (int t = 0; t < 2 * KS; t += 2) {
+                Planes<kO> a[2], d[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    a[i] = col_frag<kO, kPitch, 32>(s_buf + Sl::kS, t + i, 0, lane);
+                    d[i] = col_frag<kO, kPitch, 32>(s_buf + Sl::kDs, t + i, 0, lane);
+                }
+                mma_tiles<kO>(a, On, D1 + t);
+                mma_tiles<kO>(a, Rn, D2 + t);
+                mma_tiles<kO>(d, En, D3 + t);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (((t + i) & 3) == wave)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) bound += plane_sum(a[i], j) * plane_sum(d[i], j);
+            }
+            barrier();
+            if (sl + 1 < slabs) stage_states(sl + 1);
         }
+        wait_copies();
         barrier();
         keys(s_k, p.kr + keys.head + c * keys.step, rows);
         keys(s_q, p.qr + keys.head + c * keys.step, rows);
