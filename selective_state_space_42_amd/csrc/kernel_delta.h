@@ -113,29 +113,33 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Two values are rounded by one instruction, and what a rounding leaves is one
 // dot product with (-1, 0) or (0, -1) each, exact as the difference has at most
-// 24 bits: 3.5 instructions a value for three planes.
+// 24 bits: 3.5 instructions a value for three planes.  All eight values plane by
+// plane: a dot product's result is not ready for the next three instructions.
 template <int N>
 __device__ __forceinline__ void split8(const float (&x)[8], Planes<N>& o) {
     // in registers: as an inline constant, a packed (-1, 0) is not read as one
     uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
     asm("" : "+s"(lo), "+s"(hi));
     const bf16x2 low = __builtin_bit_cast(bf16x2, lo), high = __builtin_bit_cast(bf16x2, hi);
-    u32x4 w[N];
+    float r[8];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        float a = x[j], b = x[j + 1];
+    for (int j = 0; j < 8; ++j) r[j] = x[j];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const bf16x2 h = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
-            w[n][j / 2] = __builtin_bit_cast(uint32_t, h);
-            if (n + 1 < N) {
-                a = __builtin_amdgcn_fdot2_f32_bf16(h, low, a, false);
-                b = __builtin_amdgcn_fdot2_f32_bf16(h, high, b, false);
+    for (int n = 0; n < N; ++n) {
+        bf16x2 h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = bf16x2{static_cast<__bf16>(r[2 * j]), static_cast<__bf16>(r[2 * j + 1])};
+        u32x4 w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __builtin_bit_cast(uint32_t, h[j]);
+        o.p[n] = __builtin_bit_cast(bf16x8, w);
+        if (n + 1 < N)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r[2 * j] = __builtin_amdgcn_fdot2_f32_bf16(h[j], low, r[2 * j], false);
+                r[2 * j + 1] = __builtin_amdgcn_fdot2_f32_bf16(h[j], high, r[2 * j + 1], false);
             }
-        }
     }
-#pragma unroll
-    for (int n = 0; n < N; ++n) o.p[n] = __builtin_bit_cast(bf16x8, w[n]);
 }
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
