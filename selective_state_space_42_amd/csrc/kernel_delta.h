@@ -436,9 +436,9 @@ __device__ __forceinline__ f32x4 block_product(f32x4 a, f32x4 b, f32x4 c) {
 //
 // X = (I + A' D)^-1 A' by forward substitution over blocks of 16 steps, as an
 // inverse by powers of A' D would lose all digits for like keys: with T_I the
-// inverse of the diagonal block I (16 rows, a lane a column, each wave one
-// block), X_I = T_I (A'_I - sum_{J < I} A'_IJ D_J X_J) in fp32 matrix
-// instructions, wave w keeping column block w of X in registers.
+// inverse of the diagonal block I (16 rows, a lane a column, all four in one
+// wave), X_I = T_I (A'_I - sum_{J < I} A'_IJ D_J X_J) in fp32 matrix
+// instructions, each wave keeping one column block of X in registers.
 template <typename T, int KS, bool BWD>
 __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
     constexpr int kN = PlanesOf<T>::kIn, kP = PlanesOf<T>::kOut, kRow = kC + 4, kPitch = pitch_of<KS>();
@@ -482,15 +482,18 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
     }
     wait_copies();
     __syncthreads();
-    // rows of tile `wave` against the steps not behind them
+    // A wave's part of the triangle: the parts' sizes differ, and wave w of every
+    // workgroup sits on SIMD w, so they take turns.
+    const int part = (wave + static_cast<int>(blockIdx.x)) & 3;
+    // rows of tile `part` against the steps not behind them
     f32x4 kk[4], qk[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) kk[t] = qk[t] = zero4();
-    const int ntile = wave < 2 ? 2 : 4;
+    const int ntile = part < 2 ? 2 : 4;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-        const Planes<kN> ka = row_frag<kN, kPitch>(s_k, wave, s, lane);
-        const Planes<kN> qa = row_frag<kN, kPitch>(s_q, wave, s, lane);
+        const Planes<kN> ka = row_frag<kN, kPitch>(s_k, part, s, lane);
+        const Planes<kN> qa = row_frag<kN, kPitch>(s_q, part, s, lane);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
             if (t < ntile) {
@@ -502,50 +505,54 @@ __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
+        if (t >= ntile) continue;  // (above the diagonal, never read)
         const int j = tile_row(t, lane & 15);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = tile_row(wave, 4 * (lane >> 4) + r);
+            const int i = tile_row(part, 4 * (lane >> 4) + r);
             const float e = j <= i ? expf(static_cast<float>(s_g[i] - s_g[j])) : 0.f;
             s_a[i][j] = j < i ? kk[t][r] * e : 0.f;
             s_p[i][j] = j <= i ? qk[t][r] * e * p.scale : 0.f;
         }
     }
     __syncthreads();
-    {
-        // column lane % 16 of T: T_i = delta_i - sum_{l < i} A'_il beta_l T_l
-        const int o = 16 * wave, j = lane & 15;
+    const int q = lane >> 4, m = lane & 15;
+    if (part == 0) {
+        // block q, column m of its T: T_i = delta_i - sum_{l < i} A'_il beta_l T_l
+        const int o = 16 * q;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float acc = i == j ? 1.f : 0.f;
+            float acc = i == m ? 1.f : 0.f;
+            f32x4 a[4];
 #pragma unroll
-            for (int l = 0; l < i; ++l) acc -= s_a[o + i][o + l] * x[l];
-            if (lane < 16) s_t[wave][i][j] = acc;
+            for (int l = 0; l < i; l += 4) a[l / 4] = load4(&s_a[o + i][o + l]);
+#pragma unroll
+            for (int l = 0; l < i; ++l) acc -= a[l / 4][l % 4] * x[l];
+            s_t[q][i][m] = acc;
             x[i] = acc * s_b[o + i];
         }
     }
     __syncthreads();
-    const int q = lane >> 4, m = lane & 15;
     f32x4 X[4];
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
         X[I] = zero4();
-        if (I < wave) continue;
+        if (I < part) continue;
         f32x4 a;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r] = s_a[16 * I + 4 * q + r][16 * wave + m];
+        for (int r = 0; r < 4; ++r) a[r] = s_a[16 * I + 4 * q + r][16 * part + m];
 #pragma unroll
         for (int J = 0; J < I; ++J)
-            if (J >= wave) a = block_product(load4(&s_a[16 * I + m][16 * J + 4 * q]) * -load4(&s_b[16 * J + 4 * q]), X[J], a);
+            if (J >= part) a = block_product(load4(&s_a[16 * I + m][16 * J + 4 * q]) * -load4(&s_b[16 * J + 4 * q]), X[J], a);
         X[I] = block_product(load4(&s_t[I][m][4 * q]), a, zero4());
     }
     __syncthreads();
 #pragma unroll
     for (int I = 0; I < 4; ++I)
-        if (I >= wave)
+        if (I >= part)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s_a[16 * I + 4 * q + r][16 * wave + m] = X[I][r];
+            for (int r = 0; r < 4; ++r) s_a[16 * I + 4 * q + r][16 * part + m] = X[I][r];
     __syncthreads();
     for (int i = tid; i < 8 * 64; i += 256) {
         const int l = i & 63, t = i >> 7, s = (i >> 6) & 1;
