@@ -33,6 +33,10 @@ typedef struct {
     int32_t io_dtype;  /* ssm_dtype_t of q, k, v, g, beta, y and of their gradients */
 } ssm_delta_desc_t;
 
+/* SSM_ERR_UNSUPPORTED: K, V or Hv beyond the limits above, an unknown io_dtype,
+ * or more than 2^24 - 1 chunks of 64 steps (B * Hv * ceil(L / 64)) or groups of
+ * 32 columns (2 B * Hv * ceil(V / 32)). */
+
 /* Bytes of workspace ssm_delta_fwd and ssm_delta_bwd need for `desc`; 0 for an
  * invalid or unsupported descriptor.  Both grow with B * ceil(L / 64). */
 size_t ssm_delta_workspace_bytes(const ssm_delta_desc_t *desc);

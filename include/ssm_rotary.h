@@ -43,7 +43,10 @@ typedef struct {
  *   q_out, k_out  like q and k (written); each may be its input itself, and
  *              overlaps nothing else
  * With inverse = 1 the call maps gradients of the outputs to gradients of the
- * inputs.  The elements behind R are copied.  Returns an ssm_status_t.
+ * inputs.  The elements behind R are copied.  Returns an ssm_status_t
+ * (SSM_ERR_UNSUPPORTED for an unknown io_dtype, K beyond 65536, or a problem of
+ * more than 2^32 pieces: 16 bytes where rows and pointers are multiples of
+ * that, single elements otherwise).
  */
 int ssm_rotary(const ssm_rotary_desc_t *desc, const void *q, const void *k, const float *inv_freq,
                const int64_t *positions, void *q_out, void *k_out, void *stream);

@@ -10,7 +10,7 @@ namespace {
 
 using namespace ssm::delta;
 
-constexpr int64_t kMaxElements = int64_t(1) << 40;
+constexpr int64_t kMaxElements = int64_t(1) << 50;
 
 int check_desc(const ssm_delta_desc_t* d) {
     if (!d) return SSM_ERR_INVALID_ARGUMENT;
@@ -20,9 +20,11 @@ int check_desc(const ssm_delta_desc_t* d) {
     if (d->io_dtype != SSM_DTYPE_F32 && d->io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
     // a chunk's rows are reached by 32-bit offsets: 64 rows of at most 4096 x 1024 elements
     if (d->dkey > 128 || d->dvalue > 1024 || d->vheads > 4096) return SSM_ERR_UNSUPPORTED;
-    if (!ssm::product_fits({d->batch, d->seqlen, d->vheads, 1024}, kMaxElements) ||
-        !ssm::product_fits({d->batch, (d->seqlen + kC - 1) / kC, d->vheads, (d->dvalue + 15) / 16}, INT32_MAX))
-        return SSM_ERR_INVALID_ARGUMENT;
+    if (!ssm::product_fits({d->batch, d->seqlen, d->vheads, 1024}, kMaxElements)) return SSM_ERR_INVALID_ARGUMENT;
+    // chunks of all heads, and both sweeps' or the step's column groups of all heads, as workgroups of 256
+    if (!ssm::product_fits({d->batch, d->vheads, (d->seqlen + kC - 1) / kC}, ssm::kMaxWorkgroups) ||
+        !ssm::product_fits({d->batch, d->vheads, 2 * ((d->dvalue + 31) / 32)}, ssm::kMaxWorkgroups))
+        return SSM_ERR_UNSUPPORTED;
     return SSM_OK;
 }
 
@@ -109,7 +111,7 @@ void sweep(Params p, hipStream_t s) {
     constexpr int units = MODE == kForward ? block_units<T, false>() : 1 + kSplit;
     constexpr int lds = NBUF * Stage<T, KS, units, MODE == kForward>::kElements * 2;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
-    const int64_t cols = MODE == kForward ? p.V : MODE == kStates ? p.VP : p.vt_cols + p.kt_cols;
+    const int64_t cols = MODE == kForward ? p.V : p.vt_cols + p.kt_cols;
     p.nV = (cols + 16 * NW - 1) / (16 * NW);
     const dim3 g = grid(p.B * p.Hv * (MODE == kTransition ? p.segs - 1 : p.segs) * p.nV), block(64 * NW);
     if constexpr (sizeof(T) == 2)
@@ -121,17 +123,19 @@ void sweep(Params p, hipStream_t s) {
 }
 
 template <typename T, int KS, int NW, int NBUF>
-void adjoint(GradParams g, hipStream_t s) {
-    constexpr int lds = NBUF * Stage<T, KS, 2 * kSplit + 1, true>::kElements * 2;
+void sweeps(GradParams g, hipStream_t s) {
+    constexpr int adjoint = Stage<T, KS, 2 * kSplit + 1, true>::kElements;
+    constexpr int states = Stage<T, KS, 1 + kSplit, false>::kElements;
+    constexpr int lds = NBUF * (adjoint > states ? adjoint : states) * 2;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     g.f.nV = (g.f.VP + 16 * NW - 1) / (16 * NW);
-    const dim3 gr = grid(g.f.B * g.f.Hv * g.f.nV), block(64 * NW);
+    const dim3 gr = grid(2 * g.f.B * g.f.Hv * g.f.nV), block(64 * NW);
     if constexpr (sizeof(T) == 2)
-        if (g.vec_dy) {
-            hipLaunchKernelGGL((delta_adjoint_kernel<T, KS, NW, NBUF, true>), gr, block, lds, s, g);
+        if (g.f.vec_v && g.vec_dy) {
+            hipLaunchKernelGGL((delta_sweeps_kernel<T, KS, NW, NBUF, true>), gr, block, lds, s, g);
             return;
         }
-    hipLaunchKernelGGL((delta_adjoint_kernel<T, KS, NW, NBUF, false>), gr, block, lds, s, g);
+    hipLaunchKernelGGL((delta_sweeps_kernel<T, KS, NW, NBUF, false>), gr, block, lds, s, g);
 }
 
 template <typename T, int KS, bool BWD>
@@ -156,8 +160,7 @@ template <typename T, int KS>
 int bwd(const GradParams& g, hipStream_t s) {
     constexpr int nbuf = sizeof(T) == 4 ? 1 : 2;
     prepare<T, KS, true>(g.f, s);
-    sweep<T, KS, kStates, 4, nbuf>(g.f, s);
-    adjoint<T, KS, 4, nbuf>(g, s);
+    sweeps<T, KS, 4, nbuf>(g, s);
     const dim3 chunks = grid(g.f.B * g.f.Hk * g.f.nC);
     if (g.f.Hv > g.f.Hk)
         hipLaunchKernelGGL((delta_grad_kernel<T, KS, true>), chunks, dim3(256), 0, s, g);

@@ -14,6 +14,9 @@ int hip_status(hipError_t e);
 
 inline int launch_status() { return hip_status(hipGetLastError()); }
 
+// Workgroups of 256 threads in one launch: its threads are counted in 32 bits.
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 inline bool finite(float x) { return x - x == 0.f; }

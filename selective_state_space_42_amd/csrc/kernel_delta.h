@@ -693,17 +693,16 @@ enum Sweep : int { kForward = 0, kStates = 1, kTransition = 2 };
 // segment's end.  VT: values are staged too (bf16 rows of
 // whole 16-byte pieces).
 template <typename T, int KS, int MODE, int NW, int NBUF, bool VT>
-__global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
+__device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, int64_t workgroups, uint16_t* smem) {
     constexpr bool OUT = MODE == kForward, BWD = MODE == kStates;
     constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
     constexpr int kUnits = OUT ? block_units<T, false>() : 1 + kSplit;
     constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;  // of the state, at a time
     using St = Stage<T, KS, kUnits, OUT>;
     using Blk = Block<BWD>;
-    extern __shared__ __align__(16) uint16_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
     // column groups of a segment, segments of a head, heads
-    const int64_t block = xcd_run(blockIdx.x, gridDim.x), vt = block % p.nV, rest = block / p.nV;
+    const int64_t block = xcd_run(workgroup, workgroups), vt = block % p.nV, rest = block / p.nV;
     const int64_t segs = MODE == kTransition ? p.segs - 1 : p.segs, seg = rest % segs, bh = rest / segs;
     const int64_t VP = p.VP, b = bh / p.Hv, h = bh % p.Hv;
     const int64_t hk = h / (p.Hv / p.Hk);
@@ -925,6 +924,12 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
         store_state<KS>(p.trans + ((bh * segs + seg) * n + col) * p.K, p.K, true, lane, S);
     }
     if (OUT && p.h_last && seg == segs - 1) store_state<KS>(p.h_last + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
+}
+
+template <typename T, int KS, int MODE, int NW, int NBUF, bool VT>
+__global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
+    extern __shared__ __align__(16) uint16_t smem[];
+    chunk_sweep<T, KS, MODE, NW, NBUF, VT>(p, blockIdx.x, gridDim.x, smem);
 }
 
 // The states entering segments 1, 2, ...: with N the state a segment leaves when

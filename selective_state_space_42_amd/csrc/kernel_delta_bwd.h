@@ -5,9 +5,8 @@
 //   dU = P^T dY + e^{G_63 - G} o (K dS')
 //   dR = (I - X^T D) dU,  dE = beta o dR = dV,  dbeta = rows of dR . E^
 //   dS = e^{G_63} dS' + (scale e^G o Q)^T dY - (e^G o K)^T dE
-// runs backwards over the chunks (delta_adjoint_kernel, the mirror of
-// delta_chunk_kernel), after a forward sweep that keeps the states entering
-// the chunks and E^.  Everything else is a chunk's own (delta_grad_kernel):
+// runs backwards over the chunks, beside a forward sweep that keeps the states
+// entering the chunks and E^ (delta_sweeps_kernel).  Everything else is a chunk's own (delta_grad_kernel):
 //   W1_ij = e^{G_i - G_j} dY_i . U_j (j <= i),   W2_ij = e^{G_i - G_j} dE_i . U_j (j < i)
 //   dQ  = scale (e^G o (dY S^T) + W1 K)
 //   row = -(e^G o (dE S^T) + W2 K),   col = scale W1^T Q - W2^T K + over,  over = e^{G_63 - G} o (U dS'^T)
@@ -32,17 +31,17 @@ struct GradParams {
     int32_t vec_dy;     // rows of dy move in 16-byte pieces
 };
 
-// The mirror of delta_chunk_kernel, backwards over the chunks.
+// The mirror of chunk_sweep, backwards over the chunks.
 template <typename T, int KS, int NW, int NBUF, bool VT>
-__global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(GradParams gp) {
+__device__ __forceinline__ void adjoint_sweep(const GradParams& gp, int64_t workgroup, int64_t workgroups,
+                                              uint16_t* smem) {
     constexpr int kN = PlanesOf<T>::kIn, kPitch = pitch_of<KS>(), kUnits = 2 * kSplit + 1;
     constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;
     using St = Stage<T, KS, kUnits, true>;
     using Blk = Block<true>;
-    extern __shared__ __align__(16) uint16_t smem[];
     const Params& p = gp.f;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
-    const int64_t block = xcd_run(blockIdx.x, gridDim.x), vt = block % p.nV, bh = block / p.nV;
+    const int64_t block = xcd_run(workgroup, workgroups), vt = block % p.nV, bh = block / p.nV;
     const int64_t VP = p.VP, b = bh / p.Hv, h = bh % p.Hv;
     const int64_t hk = h / (p.Hv / p.Hk);
     const int64_t col0 = vt * 16 * NW, col = col0 + 16 * wave + (lane & 15);
@@ -54,7 +53,7 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
     const KeyCopy<T, KS, NW> keys(p, b, hk, wave, lane);
     const int64_t cols = p.V - col0;
     const RowCopy<64, NW> values(vstride, static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
-    // in six parts between the products, as in delta_chunk_kernel
+    // in six parts between the products, as in chunk_sweep
     constexpr int kThird = kUnits / 3 / NW * NW;
     const auto issue = [&](int64_t c, int part) {  // before the first chunk: empty windows
         __builtin_amdgcn_sched_barrier(0);
@@ -205,6 +204,19 @@ __global__ void __launch_bounds__(64 * NW, KS > 3 ? 1 : 2) delta_adjoint_kernel(
     }
     wait_copies();  // none may land once the workgroup's LDS is another's
     if (gp.dh0) store_state<KS>(gp.dh0 + (bh * p.V + (ok ? col : 0)) * p.K, p.K, ok, lane, S);
+}
+
+// Both sweeps of the backward pass.  Neither waits for the other, and each leaves
+// many CUs idle where heads are few: the first half of the workgroups runs the
+// longer one, the adjoint's, the second the states'.
+template <typename T, int KS, int NW, int NBUF, bool VT>
+__global__ void __launch_bounds__(64 * NW, 2) delta_sweeps_kernel(GradParams gp) {
+    extern __shared__ __align__(16) uint16_t smem[];
+    const int64_t half = gridDim.x / 2;
+    if (blockIdx.x < half)
+        adjoint_sweep<T, KS, NW, NBUF, VT>(gp, blockIdx.x, half, smem);
+    else
+        chunk_sweep<T, KS, kStates, NW, NBUF, VT>(gp.f, blockIdx.x - half, half, smem);
 }
 
 // 8 neighbours at a 16-byte boundary

@@ -41,7 +41,7 @@ int launch(const ssm_rotary_desc_t* d, ssm::rotary::Params& p, hipStream_t s) {
     int64_t blocks;
     if (__builtin_mul_overflow(rows, p.groups, &blocks)) return SSM_ERR_UNSUPPORTED;
     blocks = (blocks + 255) / 256;
-    if (blocks > INT32_MAX) return SSM_ERR_UNSUPPORTED;
+    if (blocks > ssm::kMaxWorkgroups) return SSM_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(blocks)), block(256);
     using namespace ssm::rotary;
     if (vec && d->interleaved)

@@ -63,6 +63,8 @@ def test_delta_descriptor_rules(call, L):
     for kw in [dict(K=129), dict(V=1025), dict(dtype=2)]:
         assert call(ddesc(**{"L": L, **kw})) == UNSUPPORTED, kw
     assert call(ddesc(B=1 << 30, L=1 << 30)) == INVALID
+    assert call(ddesc(B=1 << 20, Hk=16, Hv=16, L=L)) == UNSUPPORTED       # 2^24 chunks: one too many for a launch
+    assert call(ddesc(Hk=1, Hv=4097, L=L)) == UNSUPPORTED
     assert call(ddesc(B=1 << 24, Hk=1 << 10, Hv=1 << 10, L=1)) == INVALID
 
 
@@ -117,6 +119,8 @@ def test_rotary_rules():
         assert call_rotary(rdesc(**kw)) == INVALID, kw
     assert call_rotary(rdesc(dtype=3)) == UNSUPPORTED
     assert call_rotary(rdesc(K=65538)) == UNSUPPORTED
+    far = dict(k=0, k_out=0, q_out=Q + (1 << 50))
+    assert call_rotary(rdesc(B=1 << 20, L=1 << 9, Hk=0, Hq=1, K=33, R=32), **far) == UNSUPPORTED  # 2^29 x 17 pieces
     for n in ("q", "k", "inv", "q_out", "k_out"):
         assert call_rotary(rdesc(), **{n: 0}) == INVALID, n
         assert call_rotary(rdesc(), **{n: P + 2}) == INVALID, n
