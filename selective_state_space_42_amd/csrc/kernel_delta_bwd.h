@@ -369,10 +369,9 @@ __global__ void __launch_bounds__(256, GROUPED || sizeof(T) == 4 ? 1 : 2) delta_
                     mma_tiles<kO>(r, En, B2 + t);
                 }
             }
-            if (sl > 0) {  // this slab's states
-                wait_copies();
-                barrier();
-            }
+            // this slab's states and the next one's steps
+            wait_copies();
+            barrier();
 #pragma unroll
             for (int t = 0; t < 2 * KS; t += 2) {
                 Planes<kO> a[2], d[2];

@@ -65,7 +65,7 @@ def test_delta_descriptor_rules(call, L):
     assert call(ddesc(B=1 << 30, L=1 << 30)) == INVALID
     assert call(ddesc(B=1 << 20, Hk=16, Hv=16, L=L)) == UNSUPPORTED       # 2^24 chunks: one too many for a launch
     assert call(ddesc(Hk=1, Hv=4097, L=L)) == UNSUPPORTED
-    assert call(ddesc(B=1 << 24, Hk=1 << 10, Hv=1 << 10, L=1)) == INVALID
+    assert call(ddesc(B=1 << 24, Hk=1 << 10, Hv=1 << 10, L=1)) == UNSUPPORTED
 
 
 def test_delta_pointer_rules():

@@ -263,6 +263,30 @@ def test_equal_calls_give_equal_bits_whatever_the_workspace_holds(dtype):
         assert torch.equal(g1[n], g2[n]), n
 
 
+@DTYPES
+def test_rows_do_not_depend_on_what_runs_beside_them(dtype):
+    """A batch that fills the GPU several times over, bit for bit the same as
+    each of its rows by itself: copies that are read before they have landed
+    show at full load first.  (Below 32 chunks no row is swept in segments, which
+    round differently.)"""
+    B, L, Hk, Hv, K, V = 4, 1984, 20, 20, 128, 128
+    x = make(1, L, Hk, Hv, K, V, dtype, seed=95, device="cuda")
+    x = {n: torch.cat([t.roll(i, 2 if n != "h0" else 1) for i in range(B)]) for n, t in x.items()}
+    dy, dh = upstream(x, 11, dtype)
+    names = ("q", "k", "v", "g", "beta", "h0")
+    whole = scan.ssm_delta_bwd(*(x[n] for n in names), dy=dy, dh_last=dh, want_dh0=True)
+    y, h = fwd(x)
+    torch.cuda.synchronize()
+    for b in range(B):
+        one = {n: x[n][b:b + 1].contiguous() for n in names}
+        y1, h1 = fwd(one)
+        assert torch.equal(y[b:b + 1], y1) and torch.equal(h[b:b + 1], h1), b
+        part = scan.ssm_delta_bwd(*(one[n] for n in names), dy=dy[b:b + 1].contiguous(),
+                                  dh_last=dh[b:b + 1].contiguous(), want_dh0=True)
+        for n in whole:
+            assert torch.equal(whole[n][b:b + 1], part[n]), (b, n)
+
+
 def test_captured_calls_replay():
     """Forward, gradients and a step in one graph, replayed with eager work on
     the same inputs between the replays."""
