@@ -20,7 +20,8 @@
 // takes the plane pairs a_i b_j with i + j < 3: an fp32 product to 2^-24 at 3
 // (bf16 by fp32) or 6 (fp32 by fp32) times a bf16 product's cost, against 16
 // times for the fp32 matrix instruction.  bf16 inputs are one plane, exactly.
-// Only y with bf16 I/O is formed from two planes (16 bits): it is rounded to 8.
+// With bf16 I/O, y and the chunks' own gradients are formed from two planes (16
+// bits): they are rounded to 8.  States, their gradients and what feeds them keep three.
 //
 // Data flow inside a wave.  A wave owns 16 columns v of the state and keeps
 // them in accumulators through the whole sequence.  A 16x16 result leaves lane
@@ -32,9 +33,11 @@
 // and the results of tiles 2s, 2s + 1 ARE the right operand of k step s: no
 // exchange between lanes, no LDS, anywhere on the recurrence's path.
 //
-// Left operands are laid out once per chunk as fragments (1 KiB: 64 lanes x 16
-// bytes, in lane order) by delta_pack_kernel (keys and queries, per key head)
-// and delta_solve_kernel (X and P, per value head).
+// Left operands.  X and P are laid out once per chunk as fragments (1 KiB: 64
+// lanes x 16 bytes, in lane order) by delta_solve_kernel.  Keys and queries are
+// staged from the tensors as they are (bf16 rows of whole 16-byte pieces; else
+// delta_pack_kernel makes zero-padded planes of them) and read from LDS by rows
+// or, with ds_read_b64_tr_b16, transposed.
 #pragma once
 
 #include "device_common.h"
@@ -389,7 +392,8 @@ struct KeyCopy {
 };
 
 // Keys and queries in zero-padded bf16 planes, where the tensors cannot be
-// copied as they are: fp32, or rows that are not 16-byte pieces.
+// copied as they are: fp32, or rows that are not 16-byte pieces.  Bound by its
+// writes and its launch (fp32, 6 x 1021 x 5 heads of 80: 15 us for 35 MB).
 template <typename T, int KS>
 __global__ void __launch_bounds__(256) delta_pack_kernel(Params p) {
     constexpr int kN = PlanesOf<T>::kIn, kPitch = pitch_of<KS>();
@@ -439,6 +443,11 @@ __device__ __forceinline__ f32x4 block_product(f32x4 a, f32x4 b, f32x4 c) {
 // inverse of the diagonal block I (16 rows, a lane a column, all four in one
 // wave), X_I = T_I (A'_I - sum_{J < I} A'_IJ D_J X_J) in fp32 matrix
 // instructions, each wave keeping one column block of X in registers.
+//
+// Bound by its vector instructions (70 % of the issue slots, most of them the
+// decays and the splits) and by what it writes, 31 KB a chunk and head: 4 x 8192
+// steps of 20 heads of 128, bf16: 128 us, 0.49 GB, 3.8 TB/s.  As one lane a column over all
+// 64 rows (2016 dependent products in one wave) it took 488 us.
 template <typename T, int KS, bool BWD>
 __global__ void __launch_bounds__(256) delta_solve_kernel(Params p) {
     constexpr int kN = PlanesOf<T>::kIn, kP = PlanesOf<T>::kOut, kRow = kC + 4, kPitch = pitch_of<KS>();
@@ -679,7 +688,7 @@ __device__ __forceinline__ void put_planes(rsrc_t w, uint32_t slab_off, int v, i
 template <typename T, int KS, int UNITS, bool QUERIES>
 struct Stage {
     static constexpr int kTile = PlanesOf<T>::kIn * 64 * pitch_of<KS>();
-    static constexpr int kBlk = 0, kK = UNITS * kFrag, kQ = kK + kTile, kV = kQ + (QUERIES ? kTile : 0);
+    static constexpr int kK = UNITS * kFrag, kQ = kK + kTile, kV = kQ + (QUERIES ? kTile : 0);
     static constexpr int kElements = kV + (sizeof(T) == 2 ? 64 * 64 : 0);
 };
 
@@ -688,6 +697,16 @@ enum Sweep : int { kForward = 0, kStates = 1, kTransition = 2 };
 // The recurrence over chunks: one wave per 16 columns of a head's state, NW
 // waves (neighbouring columns) sharing what is staged in LDS.  With two
 // buffers the next chunk's copies run under this chunk's products.
+//
+// Bound by how fast one wave on a SIMD gets its instructions out: 182 matrix
+// and about 700 other instructions a chunk of 128 x 128, with 90 KB of LDS reads a wave, take
+// 8,400 cycles, of which the matrix unit is busy 2,900 and the LDS of a CU
+// (four waves) 4,200.  4 x 8192 steps of 20 heads of 128, bf16: 477 us for 0.83 GB; operands from global memory
+// without LDS took 2,990.  Measured and not kept: 8 waves sharing the staged
+// tiles (0.53 against 0.59 ms for the whole forward at 160 heads, but 0.51 against 0.49 at 320),
+// one buffer and two workgroups a CU (heads of 64: 341 against 319 us in all), vector
+// work dealt out by hand between the matrix instructions (504 us: more live
+// registers, more moves).
 // kForward writes y and h_last, kStates the states entering each chunk and E^
 // (what the gradients read), kTransition nothing but the states at its
 // segment's end.  VT: values are staged too (bf16 rows of
@@ -936,7 +955,8 @@ __global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
 // it starts from 0 (segment 0: from h0) and row e of M the one it leaves when it
 // starts from unit row e without values (both rows of `trans`),
 //   enter_1 = N_0,  enter_{j + 1} = N_j + enter_j M_j.
-// A workgroup takes 8 rows v of a head; thread k % 128 one key element.
+// A workgroup takes 8 rows v of a head; thread k % 128 one key element.  Bound by
+// the chain over segments, each K reads of M deep: 57 us for 20 heads of 128 x 128, 6 segments.
 __global__ void __launch_bounds__(256) delta_join_kernel(Params p) {
     __shared__ __align__(16) float s_s[8][128];
     const int tid = threadIdx.x, k = tid & 127, half = tid >> 7;  // half: rows 4 half .. 4 half + 3
@@ -979,6 +999,8 @@ __global__ void __launch_bounds__(256) delta_join_kernel(Params p) {
 // holding the float4 pieces i, i + 8, ... of its K elements (VEC; single
 // elements i, i + 8, ... otherwise); a workgroup has 32 rows of one head.  The
 // state is read once and written once: 8 V K bytes per head, all of the cost.
+// 256 x 20 heads of 128 x 128: 107 us, 6.3 TB/s (part of the state stays in the 256
+// MB cache between calls); with keys read element by element 161 us.
 struct StepParams {
     const void *q, *k, *v, *g, *beta;
     float* h;

@@ -6,6 +6,10 @@
 // The angle p inv_freq is an fp64 product (exact for |p| < 2^29), reduced in
 // fp64: fp32 accuracy at any position.  Elements behind R are copied by
 // further items of the same row.  q and k heads are one list of heads.
+//
+// Bound by memory, each element read and written once: 4 x 8192 x 20 heads of
+// 128, bf16: 69 us, 4.9 TB/s, a copy's rate; 131,072 x 24 heads, half turned: 336 us, 4.8
+// TB/s.  Non-temporal accesses measured 65 and 389 us and were not kept.
 #pragma once
 
 #include "device_common.h"
