@@ -22,6 +22,7 @@ int check_desc(const ssm_delta_desc_t* d) {
     if (d->dkey > 128 || d->dvalue > 1024 || d->vheads > 4096) return SSM_ERR_UNSUPPORTED;
     if (!ssm::product_fits({d->batch, d->seqlen, d->vheads, 1024}, kMaxElements)) return SSM_ERR_INVALID_ARGUMENT;
     // chunks of all heads, and both sweeps' or the step's column groups of all heads, as workgroups of 256
+    // (the sweep of the forward, of 320, has half as many as the last)
     if (!ssm::product_fits({d->batch, d->vheads, (d->seqlen + kC - 1) / kC}, ssm::kMaxWorkgroups) ||
         !ssm::product_fits({d->batch, d->vheads, 2 * ((d->dvalue + 31) / 32)}, ssm::kMaxWorkgroups))
         return SSM_ERR_UNSUPPORTED;
@@ -38,8 +39,8 @@ int64_t key_steps(const ssm_delta_desc_t* d) { return (d->dkey + 31) / 32; }
 // a head's chunks one by one and has a workgroup of 4 waves for 64 columns of
 // a head, so few heads leave most of the 256 CUs idle.  Segments cost a sweep more (each one's
 // transition: V + K columns, without outputs), which pays from about 4 on.
-// (32,768 steps of 20 heads of 128, bf16: 1.86 ms as one segment, 0.87 in 6,
-// 0.92 in 12.)
+// (32,768 steps of 20 heads of 128, bf16: before a wave of
+// their own issued the forward's copies 1.86 ms as one segment, 0.87 in 6, 0.92 in 12.)
 int64_t segments(const ssm_delta_desc_t* d) {
     const int64_t groups = d->batch * d->vheads * ((d->dvalue + 63) / 64), chunks = (d->seqlen + kC - 1) / kC;
     int64_t n = 256 / groups;
@@ -113,7 +114,8 @@ void sweep(Params p, hipStream_t s) {
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     const int64_t cols = MODE == kForward ? p.V : p.vt_cols + p.kt_cols;
     p.nV = (cols + 16 * NW - 1) / (16 * NW);
-    const dim3 g = grid(p.B * p.Hv * (MODE == kTransition ? p.segs - 1 : p.segs) * p.nV), block(64 * NW);
+    const dim3 g = grid(p.B * p.Hv * (MODE == kTransition ? p.segs - 1 : p.segs) * p.nV);
+    const dim3 block(64 * (NW + has_loader(MODE, NBUF)));
     if constexpr (sizeof(T) == 2)
         if (p.vec_v) {
             hipLaunchKernelGGL((delta_chunk_kernel<T, KS, MODE, NW, NBUF, true>), g, block, lds, s, p);

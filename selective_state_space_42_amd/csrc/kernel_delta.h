@@ -694,19 +694,29 @@ struct Stage {
 
 enum Sweep : int { kForward = 0, kStates = 1, kTransition = 2 };
 
+// Whether one more wave of the workgroup, the loader, issues a sweep's copies: a
+// wave is held up until the copies before its own are under way, which costs
+// waves that compute too 850 cycles a chunk (4 x 8192 steps of 20 heads of 128,
+// bf16: the sweep 477 us, with a loader 429).  With one buffer nothing could
+// run beside the copies, and the states' sweep shares its launch with the
+// adjoint's, which a loader does not help (4 x 4096: 919 us for all gradients,
+// 952 with one).
+__host__ __device__ constexpr bool has_loader(int mode, int nbuf) { return mode == kForward && nbuf == 2; }
+
 // The recurrence over chunks: one wave per 16 columns of a head's state, NW
 // waves (neighbouring columns) sharing what is staged in LDS.  With two
 // buffers the next chunk's copies run under this chunk's products.
 //
 // Bound by how fast one wave on a SIMD gets its instructions out: 182 matrix
 // and about 700 other instructions a chunk of 128 x 128, with 90 KB of LDS reads a wave, take
-// 8,400 cycles, of which the matrix unit is busy 2,900 and the LDS of a CU
-// (four waves) 4,200.  4 x 8192 steps of 20 heads of 128, bf16: 477 us for 0.83 GB; operands from global memory
+// 7,550 cycles, of which the matrix unit is busy 2,900 and the LDS of a CU
+// (four waves) 4,200.  4 x 8192 steps of 20 heads of 128, bf16: 429 us for 0.83 GB; operands from global memory
 // without LDS took 2,990.  Measured and not kept: 8 waves sharing the staged
 // tiles (0.53 against 0.59 ms for the whole forward at 160 heads, but 0.51 against 0.49 at 320),
 // one buffer and two workgroups a CU (heads of 64: 341 against 319 us in all), vector
-// work dealt out by hand between the matrix instructions (504 us: more live
-// registers, more moves).
+// work dealt out by hand between the matrix instructions (504 against 484 us: more live
+// registers, more moves), three computing waves beside the loader, so that each
+// has a SIMD to itself (500 against 505 us in all).
 // kForward writes y and h_last, kStates the states entering each chunk and E^
 // (what the gradients read), kTransition nothing but the states at its
 // segment's end.  VT: values are staged too (bf16 rows of
@@ -717,6 +727,8 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
     constexpr int kN = PlanesOf<T>::kIn, kO = PlanesOf<T>::kOut, kPitch = pitch_of<KS>();
     constexpr int kUnits = OUT ? block_units<T, false>() : 1 + kSplit;
     constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;  // of the state, at a time
+    constexpr bool kLoad = has_loader(MODE, NBUF), kSpread = NBUF == 2 && !kLoad;
+    constexpr int kCopiers = kLoad ? 1 : NW;
     using St = Stage<T, KS, kUnits, OUT>;
     using Blk = Block<BWD>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
@@ -738,13 +750,14 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
     static_assert(!VT || sizeof(T) == 2, "a tile of values is one bf16 plane");
     const uint32_t ystep = static_cast<uint32_t>(vstride * sizeof(T));
 
-    const KeyCopy<T, KS, NW> keys(p, b, hk, wave, lane);
+    const int copier = kLoad ? 0 : wave;
+    const KeyCopy<T, KS, kCopiers> keys(p, b, hk, copier, lane);
     const int64_t cols = p.V - col0;
-    const RowCopy<64, NW> values(vstride, unit ? 0 : static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), wave, lane);
-    // a chunk's copies in five parts, placed between the products: all at once
-    // they would hold up the wave until the copies before them are under way
-    // (18 a wave: 2,000 of 9,700 cycles a chunk)
-    constexpr int kHalf = kUnits / 2 / NW * NW;
+    const RowCopy<64, kCopiers> values(vstride, unit ? 0 : static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), copier,
+                                       lane);
+    // a chunk's copies in five parts: waves that compute too place them between
+    // the products (all at once, 18 a wave, they hold it up for 2,000 cycles)
+    constexpr int kHalf = kUnits / 2 / kCopiers * kCopiers;
     const uint16_t* blk = p.blk + ((bh * p.nC + c0) * block_units<T, BWD>() + Blk::kVec) * kFrag;
     const int64_t head = keys.head + c0 * keys.step;
     const uint16_t *kr = p.kr + head, *qr = p.qr + head;
@@ -755,8 +768,8 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
     const auto issue = [&](int part) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
         if (part == 0) keys(st_next + St::kK, kr, rows);
-        if (part == 1) stage_block<0, kHalf, NW>(st_next, blk, rows > 0, wave, lane);
-        if (part == 2) stage_block<kHalf, kUnits, NW>(st_next, blk, rows > 0, wave, lane);
+        if (part == 1) stage_block<0, kHalf, kCopiers>(st_next, blk, rows > 0, copier, lane);
+        if (part == 2) stage_block<kHalf, kUnits, kCopiers>(st_next, blk, rows > 0, copier, lane);
         if constexpr (VT)
             if (part == 3) values(st_next + St::kV, vr, rows);
         if constexpr (OUT)
@@ -776,6 +789,18 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
         vr += kC * vstride;
         if constexpr (NBUF == 2) st_next = smem + ((c + 1 - c0) & 1) * St::kElements;
     };
+    if constexpr (kLoad)
+        if (wave == NW) {
+            // a chunk ahead: its buffer's last readers have passed the barrier
+            if (chunks > c0) issue_all();
+            for (int64_t c = c0; c < chunks; ++c) {
+                wait_copies();
+                barrier();
+                advance(c);
+                if (rows > 0) issue_all();
+            }
+            return;
+        }
 
     f32x4 S[2 * KS];
     {
@@ -813,9 +838,11 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
     const uint32_t slab_off = BWD && col < VP ? static_cast<uint32_t>(col / 32) * (Sl::kElements * 2) : kNowhere;
     const uint32_t slab_bytes = static_cast<uint32_t>(VP / 32) * (Sl::kElements * 2);
     const int slab_row = static_cast<int>(col % 32);
-    if (NBUF == 2 && chunks > c0) issue_all();
+    if (kSpread && chunks > c0) issue_all();
     for (int64_t c = c0; c < chunks; ++c) {
-        if constexpr (NBUF == 2) {
+        if constexpr (kLoad) {
+            barrier();
+        } else if constexpr (NBUF == 2) {
             wait_copies();
             barrier();
             advance(c);
@@ -844,7 +871,7 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
             split8<3>(x, Sp[s]);
             if constexpr (BWD) put_planes<kO, kPitch>(ws, slab_off, slab_row, Sl::kS, 4 * s + q, Sp[s]);
         }
-        if constexpr (NBUF == 2) {
+        if constexpr (kSpread) {
             issue(3);
             issue(4);
         }
@@ -857,7 +884,7 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
             for (int t = 0; t < 4; ++t) a[t] = row_frag<kN, kPitch>(st + St::kK, t, s, lane);
             mma_tiles<3>(a, Sp[s], acc);
         }
-        if constexpr (NBUF == 2) issue(1);
+        if constexpr (kSpread) issue(1);
         float E[2][8], be[2][8];
         Planes<3> Y[2];
 #pragma unroll
@@ -883,7 +910,7 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
             mma_tiles<3>(a, Y[0], acc);
             mma_tiles<3>(a2, Y[1], acc + 2);
         }
-        if constexpr (NBUF == 2) issue(2);
+        if constexpr (kSpread) issue(2);
         Planes<kO> U[2];
         Planes<3> W[2];
 #pragma unroll
@@ -936,7 +963,7 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
             mma_tiles<kO>(U[1], a2, out + 2);
         }
     }
-    wait_copies();  // none may land once the workgroup's LDS is another's
+    if constexpr (!kLoad) wait_copies();  // none may land once the workgroup's LDS is another's
     if (OUT && chunks > c0) put_out(chunks - 1);
     if (MODE == kTransition) {
         const int64_t n = p.vt_cols + p.kt_cols;
@@ -946,7 +973,7 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
 }
 
 template <typename T, int KS, int MODE, int NW, int NBUF, bool VT>
-__global__ void __launch_bounds__(64 * NW, 2) delta_chunk_kernel(Params p) {
+__global__ void __launch_bounds__(64 * (NW + has_loader(MODE, NBUF)), 2) delta_chunk_kernel(Params p) {
     extern __shared__ __align__(16) uint16_t smem[];
     chunk_sweep<T, KS, MODE, NW, NBUF, VT>(p, blockIdx.x, gridDim.x, smem);
 }
