@@ -124,14 +124,26 @@ void sweep(Params p, hipStream_t s) {
     hipLaunchKernelGGL((delta_chunk_kernel<T, KS, MODE, NW, NBUF, false>), g, block, lds, s, p);
 }
 
+// Whether the states' half of delta_sweeps_kernel takes 8 waves (128 columns) a
+// workgroup.  Two waves on a SIMD take less than twice a wave's time, but more
+// than one alone, and a CU holds one workgroup: this pays where it saves a round of 256.
+// (2048 steps of heads of 128, bf16, all gradients, 4 | 8 waves: 80 heads, 2 | 1 rounds, 451 | 431 us;
+// 160 heads, 3 | 2, 832 | 820; but 60 heads, 1 | 1, 375 | 394; 100 heads, 2 | 2, 559 | 609;
+// 120 heads, 2 | 2, 647 | 718.  fp32: 80 heads 1067 | 1029, 120 heads 1584 | 1663.)
+bool states_by_eight(const Params& p) {
+    const int64_t heads = p.B * p.Hv, four = (p.VP + 63) / 64, eight = (p.VP + 127) / 128;
+    return (heads * (four + eight) + 255) / 256 < (heads * 2 * four + 255) / 256;
+}
+
+// NW: waves of the states' half; the adjoint's takes 4
 template <typename T, int KS, int NW, int NBUF>
 void sweeps(GradParams g, hipStream_t s) {
     constexpr int adjoint = Stage<T, KS, 2 * kSplit + 1, true>::kElements;
-    constexpr int states = Stage<T, KS, 1 + kSplit, false>::kElements;
+    constexpr int states = Stage<T, KS, 1 + kSplit, false, NW>::kElements;
     constexpr int lds = NBUF * (adjoint > states ? adjoint : states) * 2;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
-    g.f.nV = (g.f.VP + 16 * NW - 1) / (16 * NW);
-    const dim3 gr = grid(2 * g.f.B * g.f.Hv * g.f.nV), block(64 * NW);
+    g.f.nV = (g.f.VP + 63) / 64;  // of the adjoint's sweep
+    const dim3 gr = grid(g.f.B * g.f.Hv * (g.f.nV + (g.f.VP + 16 * NW - 1) / (16 * NW))), block(64 * NW);
     if constexpr (sizeof(T) == 2)
         if (g.f.vec_v && g.vec_dy) {
             hipLaunchKernelGGL((delta_sweeps_kernel<T, KS, NW, NBUF, true>), gr, block, lds, s, g);
@@ -162,7 +174,10 @@ template <typename T, int KS>
 int bwd(const GradParams& g, hipStream_t s) {
     constexpr int nbuf = sizeof(T) == 4 ? 1 : 2;
     prepare<T, KS, true>(g.f, s);
-    sweeps<T, KS, 4, nbuf>(g, s);
+    if (states_by_eight(g.f))
+        sweeps<T, KS, 8, nbuf>(g, s);
+    else
+        sweeps<T, KS, 4, nbuf>(g, s);
     const dim3 chunks = grid(g.f.B * g.f.Hk * g.f.nC);
     if (g.f.Hv > g.f.Hk)
         hipLaunchKernelGGL((delta_grad_kernel<T, KS, true>), chunks, dim3(256), 0, s, g);

@@ -302,7 +302,9 @@ struct RowCopy {
         const u32x4 w = window(src, static_cast<uint32_t>(rows) * step);
         const uint32_t at = lds_offset(dst) + first;
 #pragma unroll
-        for (int i = 0; i < 64 / kPer; i += NW) copy16(at + i * 1024, w, lane_off[(i * kPer >> 3) & 3] + i * kPer * step);
+        for (int i = 0; i < 64 / kPer; i += NW)
+            if (i + NW <= 64 / kPer || first < (64 / kPer - i) * 1024u)
+                copy16(at + i * 1024, w, lane_off[(i * kPer >> 3) & 3] + i * kPer * step);
     }
 };
 
@@ -314,6 +316,11 @@ __device__ __forceinline__ void stage_block(uint16_t* dst, const uint16_t* src, 
 #pragma unroll
     for (int i = FROM; i < UNITS; i += NW)
         if (i + NW <= UNITS || wave < UNITS - i) copy16(at + i * 1024, w, i * 1024 + off);
+}
+
+// pieces of a row of values in a tile's 64 columns, `cols` of them before the last
+__device__ __forceinline__ int tile_pieces(int64_t cols) {
+    return static_cast<int>(cols < 0 ? 0 : cols < 64 ? cols : 64) / 8;
 }
 
 // Left operand whose rows are the 16 steps of tile t, k = elements 32 s ..
@@ -684,12 +691,12 @@ __device__ __forceinline__ void put_planes(rsrc_t w, uint32_t slab_off, int v, i
 }
 
 // What a workgroup of the sweeps keeps in LDS for one chunk, in elements.  `blk`
-// units of 1 KiB, one tile of values (bf16 only), keys, queries (where read).
-template <typename T, int KS, int UNITS, bool QUERIES>
+// units of 1 KiB, keys, queries (where read), a tile of values for every four waves (bf16 only).
+template <typename T, int KS, int UNITS, bool QUERIES, int NW = 4>
 struct Stage {
     static constexpr int kTile = PlanesOf<T>::kIn * 64 * pitch_of<KS>();
     static constexpr int kK = UNITS * kFrag, kQ = kK + kTile, kV = kQ + (QUERIES ? kTile : 0);
-    static constexpr int kElements = kV + (sizeof(T) == 2 ? 64 * 64 : 0);
+    static constexpr int kElements = kV + (sizeof(T) == 2 ? NW / 4 * 64 * 64 : 0);
 };
 
 enum Sweep : int { kForward = 0, kStates = 1, kTransition = 2 };
@@ -729,11 +736,12 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
     constexpr int kTiles = kN > 1 ? 2 : 2 * KS % 4 ? 2 : 4;  // of the state, at a time
     constexpr bool kLoad = has_loader(MODE, NBUF), kSpread = NBUF == 2 && !kLoad;
     constexpr int kCopiers = kLoad ? 1 : NW;
-    using St = Stage<T, KS, kUnits, OUT>;
+    using St = Stage<T, KS, kUnits, OUT, NW>;
     using Blk = Block<BWD>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
     // column groups of a segment, segments of a head, heads
-    const int64_t block = xcd_run(workgroup, workgroups), vt = block % p.nV, rest = block / p.nV;
+    const int64_t nV = BWD ? (p.VP + 16 * NW - 1) / (16 * NW) : p.nV;
+    const int64_t block = xcd_run(workgroup, workgroups), vt = block % nV, rest = block / nV;
     const int64_t segs = MODE == kTransition ? p.segs - 1 : p.segs, seg = rest % segs, bh = rest / segs;
     const int64_t VP = p.VP, b = bh / p.Hv, h = bh % p.Hv;
     const int64_t hk = h / (p.Hv / p.Hk);
@@ -753,8 +761,8 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
     const int copier = kLoad ? 0 : wave;
     const KeyCopy<T, KS, kCopiers> keys(p, b, hk, copier, lane);
     const int64_t cols = p.V - col0;
-    const RowCopy<64, kCopiers> values(vstride, unit ? 0 : static_cast<int>((cols < 16 * NW ? cols : 16 * NW) / 8), copier,
-                                       lane);
+    const RowCopy<64, kCopiers> values(vstride, unit ? 0 : tile_pieces(cols), copier, lane);
+    const RowCopy<64, kCopiers> values2(vstride, tile_pieces(cols - 64), copier, lane);  // of waves 4 .. 7
     // a chunk's copies in five parts: waves that compute too place them between
     // the products (all at once, 18 a wave, they hold it up for 2,000 cycles)
     constexpr int kHalf = kUnits / 2 / kCopiers * kCopiers;
@@ -771,7 +779,10 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
         if (part == 1) stage_block<0, kHalf, kCopiers>(st_next, blk, rows > 0, copier, lane);
         if (part == 2) stage_block<kHalf, kUnits, kCopiers>(st_next, blk, rows > 0, copier, lane);
         if constexpr (VT)
-            if (part == 3) values(st_next + St::kV, vr, rows);
+            if (part == 3) {
+                values(st_next + St::kV, vr, rows);
+                if constexpr (NW > 4) values2(st_next + St::kV + 64 * 64, vr + 64, rows);
+            }
         if constexpr (OUT)
             if (part == 4) keys(st_next + St::kQ, qr, rows);
         __builtin_amdgcn_sched_barrier(0);
@@ -858,7 +869,8 @@ __device__ __forceinline__ void chunk_sweep(const Params& p, int64_t workgroup, 
         const uint16_t* st = smem + (NBUF == 2 ? ((c - c0) & 1) * St::kElements : 0);
         const float* vec = reinterpret_cast<const float*>(st);
         float v8[2][8];
-        column_values<T, VT>(v8, st + St::kV, v + c * kC * vstride, len - c * kC, ystep, ok ? col : -1, wave, lane);
+        column_values<T, VT>(v8, st + St::kV + wave / 4 * (64 * 64), v + c * kC * vstride, len - c * kC, ystep,
+                             ok ? col : -1, wave % 4, lane);
         const uint16_t *xf = st + kFrag, *pf = st + (1 + kSplit) * kFrag;
         const int64_t bhc = bh * p.nC + c;
         const rsrc_t ws = buffer(!BWD ? nullptr : p.slab + bhc * (slab_bytes / 2), slab_bytes);

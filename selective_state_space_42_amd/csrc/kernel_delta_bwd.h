@@ -207,19 +207,20 @@ __device__ __forceinline__ void adjoint_sweep(const GradParams& gp, int64_t work
 }
 
 // Both sweeps of the backward pass.  Neither waits for the other, and each leaves
-// many CUs idle where heads are few: the first half of the workgroups runs the
-// longer one, the adjoint's, the second the states'.  (A chunk of the adjoint takes
-// 13,500 cycles, one of the states 9,000, both as chunk_sweep's forward bound by one wave's
-// instruction stream.)  4 x 4096 steps of 20 heads of 128, bf16: 495 us for 1.8 GB,
-// 1.1 of them the slabs; one after the other 610.
+// many CUs idle where heads are few: the first workgroups run the longer one,
+// the adjoint's, by 4 waves (the others end at once), the rest the states', by
+// NW.  (A chunk of the adjoint takes 13,500 cycles, one of the states by 4 waves
+// 9,000, both as chunk_sweep's forward bound by one wave's instruction stream.)
+// 4 x 4096 steps of 20 heads of 128, bf16: 445 us for 1.8 GB, 1.1 of them the
+// slabs; with 4 waves for the states 495, one after the other 610.
 template <typename T, int KS, int NW, int NBUF, bool VT>
 __global__ void __launch_bounds__(64 * NW, 2) delta_sweeps_kernel(GradParams gp) {
     extern __shared__ __align__(16) uint16_t smem[];
-    const int64_t half = gridDim.x / 2;
-    if (blockIdx.x < half)
-        adjoint_sweep<T, KS, NW, NBUF, VT>(gp, blockIdx.x, half, smem);
-    else
-        chunk_sweep<T, KS, kStates, NW, NBUF, VT>(gp.f, blockIdx.x - half, half, smem);
+    const int64_t adjoints = gp.f.B * gp.f.Hv * gp.f.nV;
+    if (blockIdx.x >= adjoints)
+        chunk_sweep<T, KS, kStates, NW, NBUF, VT>(gp.f, blockIdx.x - adjoints, gridDim.x - adjoints, smem);
+    else if (NW == 4 || threadIdx.x < 256)
+        adjoint_sweep<T, KS, 4, NBUF, VT>(gp, blockIdx.x, adjoints, smem);
 }
 
 // 8 neighbours at a 16-byte boundary

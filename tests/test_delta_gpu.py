@@ -264,6 +264,16 @@ def test_equal_calls_give_equal_bits_whatever_the_workspace_holds(dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("B,Hk,Hv,K,V", [(2, 20, 40, 20, 72), (5, 8, 16, 33, 100), (3, 15, 30, 64, 136), (2, 40, 40, 100, 97)])
+def test_gradients_of_many_heads(B, Hk, Hv, K, V, dtype):
+    """Counts of heads at which the states' sweep takes 128 columns a workgroup:
+    a partly filled half, one without columns, rows that are copied and rows that are not."""
+    lengths = torch.tensor([150, 70, 0, 64, 129][:B], dtype=torch.int32)
+    x = make(B, 150, Hk, Hv, K, V, dtype, seed=K, device="cuda")
+    check_bwd(x, dtype, *upstream(x, V, dtype), lengths=lengths)
+
+
+@DTYPES
 def test_rows_do_not_depend_on_what_runs_beside_them(dtype):
     """A batch that fills the GPU several times over, bit for bit the same as
     each of its rows by itself: copies that are read before they have landed
